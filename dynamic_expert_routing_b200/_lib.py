@@ -18,6 +18,7 @@ BEAM_ERR_RANGE = 7
 
 BEAM_DTYPE_F32 = 0
 BEAM_DTYPE_BF16 = 1
+BEAM_DTYPE_F16 = 2
 
 BEAM_MASK_OFF = 0x1
 BEAM_PATH_STREAM = 0x2
@@ -115,6 +116,20 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.beam_moe_backward_router.argtypes = [P, P, P, I, ctypes.c_float, P, P, P, P, P, P, P]
     lib.beam_softtopk_forward.argtypes = [P, I, I, I, ctypes.c_float, P, P, P, P]
     lib.beam_softtopk_backward.argtypes = [P, P, I, I, ctypes.c_float, P, P]
+    Q, Fl = ctypes.c_int64, ctypes.c_float
+    lib.beam_balance_workspace.argtypes = [I, I, I]
+    lib.beam_balance_workspace.restype = Q
+    lib.beam_balance_forward.argtypes = [P, I, I, I, Q, P, I, P, P, I, P, P, P, P, P, Q, P]
+    lib.beam_balance_backward.argtypes = [P, I, I, I, Q, P, I, P, P, I, P, P, Fl, P, P, P, P]
+    lib.beam_checkpoint_save.argtypes = [P, I, Q, I, Q, P, P, P]
+    lib.beam_checkpoint_load.argtypes = [P, P, Q, I, P, I, P]
+    lib.beam_checkpoint_route_grad.argtypes = [P, P, I, I, I, P, P, P, I, Q, I, Fl, P, P, P, P]
+    lib.beam_router_weight_grad.argtypes = [P, P, I, I, P, I, Q, I, I, P, P]
+    lib.beam_router_input_grad.argtypes = [P, I, Q, I, I, P, I, Q, I, P, P]
+    for f in (lib.beam_balance_forward, lib.beam_balance_backward, lib.beam_checkpoint_save,
+              lib.beam_checkpoint_load, lib.beam_checkpoint_route_grad,
+              lib.beam_router_weight_grad, lib.beam_router_input_grad):
+        f.restype = ctypes.c_int
     lib.beam_softtopk_forward.restype = ctypes.c_int
     lib.beam_softtopk_backward.restype = ctypes.c_int
     lib.beam_moe_create_ep.argtypes = [ctypes.POINTER(BeamConfig), ctypes.POINTER(BeamWeights), P,

@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import os
+import re
 import subprocess
 import sys
 
@@ -9,13 +10,14 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libbeam_moe.so")
-MAIN = os.path.join(CSRC, "beam_moe.cu")
+UNITS = [os.path.join(CSRC, f) for f in ("beam_moe.cu", "train_ops.cu")]
+OBJ = os.path.join(HERE, "_build")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
     "-gencode", "arch=compute_100a,code=sm_100a",
-    "-shared", "-Xcompiler", "-fPIC",
+    "-Xcompiler", "-fPIC",
     "-I", os.path.join(ROOT, "include"),
 ]
 
@@ -28,22 +30,54 @@ def sources():
     return out
 
 
-def stale() -> bool:
-    if not os.path.exists(LIB):
+def _older(target: str, files) -> bool:
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(s) > t for s in sources())
+    t = os.path.getmtime(target)
+    return any(os.path.getmtime(s) > t for s in files)
+
+
+def stale() -> bool:
+    return _older(LIB, sources())
+
+
+def _included(unit: str):
+    """The headers a unit includes, directly or through another header, and the unit itself."""
+    todo, seen = [unit], set()
+    while todo:
+        f = todo.pop()
+        if f in seen or not os.path.exists(f):
+            continue
+        seen.add(f)
+        for name in re.findall(r'^#include "([^"]+)"', open(f).read(), re.M):
+            todo.append(os.path.normpath(os.path.join(CSRC, name)))
+    return sorted(seen)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile the units whose sources changed (side by side), then link the library."""
     if not force and not stale():
         return LIB
+    os.makedirs(OBJ, exist_ok=True)
+    jobs, objs = [], []
+    for unit in UNITS:
+        obj = os.path.join(OBJ, os.path.basename(unit)[:-3] + ".o")
+        objs.append(obj)
+        if not force and not _older(obj, _included(unit)):
+            continue
+        tmp = obj + f".tmp{os.getpid()}"
+        cmd = [NVCC, *NVCC_FLAGS, "-c", "-o", tmp, unit]
+        if verbose:
+            cmd.insert(1, "-Xptxas=-v")
+            print(" ".join(cmd), flush=True)
+        jobs.append((subprocess.Popen(cmd), cmd, tmp, obj))
+    failed = [cmd for proc, cmd, _, _ in jobs if proc.wait() != 0]
+    if failed:
+        raise subprocess.CalledProcessError(1, failed[0])
+    for _, _, tmp, obj in jobs:
+        os.replace(tmp, obj)
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [NVCC, *NVCC_FLAGS, "-o", tmp, MAIN]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-        print(" ".join(cmd), flush=True)
-    subprocess.check_call(cmd)
+    subprocess.check_call([NVCC, "-shared", "-gencode", "arch=compute_100a,code=sm_100a", "-o", tmp, *objs])
     os.replace(tmp, LIB)
     return LIB
 

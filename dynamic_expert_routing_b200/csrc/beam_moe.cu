@@ -21,6 +21,7 @@
 #include <vector>
 
 #include "../../include/beam_moe.h"
+#include "host.cuh"
 #include "common.cuh"
 #include "router.cuh"
 #include "compact.cuh"
@@ -44,6 +45,17 @@ static beam_status_t fail(beam_status_t st, const char* fmt, ...)
     va_end(ap);
     return st;
 }
+
+// The same for the other translation units (host.cuh).
+beam_status_t beam_host_fail(beam_status_t st, const char* fmt, ...)
+{
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof g_err, fmt, ap);
+    va_end(ap);
+    return st;
+}
+void beam_host_clear_error() { g_err[0] = 0; }
 
 #define BEAM_CUDA(call)                                                                   \
     do {                                                                                  \
@@ -773,6 +785,17 @@ static void trace(const char* fmt, ...)
     fputc('\n', stderr);
     fflush(stderr);
     va_end(ap);
+}
+
+void beam_host_trace(const char* fmt, ...)
+{
+    if (!trace_on()) return;
+    char line[256];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(line, sizeof line, fmt, ap);
+    va_end(ap);
+    trace("%s", line);
 }
 
 template <typename... KArgs, typename... Args>

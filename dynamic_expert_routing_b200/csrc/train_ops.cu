@@ -1,0 +1,315 @@
+// train_ops.cu -- C ABI of the training operators that belong to no handle: the load-balance loss,
+// 8-bit activation checkpoints, the routing's slot gradients from a checkpoint and the router's
+// linear backward.  Every call enqueues its kernels on the given stream and allocates nothing;
+// scratch comes from the caller.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "host.cuh"
+#include "balance.cuh"
+#include "checkpoint.cuh"
+#include "ckpt_route_grad.cuh"
+#include "router_linear.cuh"
+
+using namespace beam;
+
+#define FAIL_ARG(...) return beam_host_fail(BEAM_ERR_INVALID_ARG, __VA_ARGS__)
+#define TRY(call)                                \
+    do {                                         \
+        const beam_status_t s_ = (call);         \
+        if (s_ != BEAM_OK) return s_;            \
+    } while (0)
+
+constexpr int kMaxExperts = 256, kMaxSlots = 32, kMaxWidth = 65536, kMaxLogits = 1 << 20;
+
+static long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+static long long align256(long long n) { return (n + 255) & ~255LL; }
+
+static int elem_size(int dtype)
+{
+    return dtype == BEAM_DTYPE_F32 ? 4 : (dtype == BEAM_DTYPE_BF16 || dtype == BEAM_DTYPE_F16) ? 2 : 0;
+}
+static bool misaligned(const void* p, int a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+// A row-major input of `rows` rows of `cols` values, rows ld apart.
+static beam_status_t check_matrix(const char* name, const void* p, int dtype, bool f16, long long rows,
+                                  long long cols, long long ld)
+{
+    if (!elem_size(dtype) || (dtype == BEAM_DTYPE_F16 && !f16))
+        FAIL_ARG("%s: unsupported data type %d", name, dtype);
+    if (ld < cols) FAIL_ARG("%s: row stride %lld is below its %lld columns", name, ld, cols);
+    if (rows > 0 && cols > 0 && !p) FAIL_ARG("%s is NULL", name);
+    if (misaligned(p, elem_size(dtype))) FAIL_ARG("%s is not aligned to its elements", name);
+    return BEAM_OK;
+}
+
+static beam_status_t check_ckpt(const int8_t* q, const uint8_t* scale, long long rows, int d)
+{
+    if (d < 1 || d > kMaxWidth) FAIL_ARG("checkpoint: d=%d must be in [1, %d]", d, kMaxWidth);
+    if (rows < 0 || rows > (1LL << 31) - 1) FAIL_ARG("checkpoint: %lld rows are out of range", rows);
+    if (rows > 0 && (!q || !scale)) FAIL_ARG("checkpoint: q or scale is NULL");
+    if (misaligned(q, 16)) FAIL_ARG("checkpoint: q must be 16-byte aligned");
+    return BEAM_OK;
+}
+
+// Calls f(T()) with the C++ type of a data type that check_matrix accepted.
+template <typename F>
+static cudaError_t with_type(int dtype, F f)
+{
+    if (dtype == BEAM_DTYPE_F32) return f(float());
+    return f(__nv_bfloat16());
+}
+template <typename F>
+static cudaError_t with_type3(int dtype, F f)
+{
+    if (dtype == BEAM_DTYPE_F16) return f(__half());
+    return with_type(dtype, f);
+}
+
+// ---------------------------------------------------------------- balance loss
+struct BalArgs {
+    const void* logits; int dtype, T, E; long long ldl; const int32_t* topk; int K;
+    const uint8_t* valid; const int32_t* cu; int n_seq;
+};
+
+static beam_status_t check_balance(const BalArgs& a)
+{
+    if (a.T < 0) FAIL_ARG("T=%d is negative", a.T);
+    if (a.E < 1 || a.E > kMaxExperts) FAIL_ARG("E=%d must be in [1, %d]", a.E, kMaxExperts);
+    if (a.K < 1 || a.K > kMaxSlots) FAIL_ARG("K=%d must be in [1, %d]", a.K, kMaxSlots);
+    if (a.cu ? (a.n_seq < 1 || a.n_seq > 65536) : a.n_seq != 0)
+        FAIL_ARG("n_seq=%d: 1 to 65536 sequences with cu_seqlens, 0 without", a.n_seq);
+    TRY(check_matrix("logits", a.logits, a.dtype, false, a.T, a.E, a.ldl));
+    if (a.T > 0 && !a.topk) FAIL_ARG("topk_id is NULL");
+    if (misaligned(a.topk, 4) || misaligned(a.cu, 4)) FAIL_ARG("the int32 arrays must be 4-byte aligned");
+    return BEAM_OK;
+}
+
+static long long bal_runs(int T) { return std::max(1LL, ceil_div(T, kBalRun)); }
+
+// Workspace: part_p, part_c [slots][E], part_n [slots], the groups' losses, the ticket.
+struct BalWork { long long slots, p, c, n, lg, ticket, bytes; };
+static BalWork bal_work(int T, int E, int n_seq)
+{
+    BalWork w;
+    const int G = std::max(1, n_seq);
+    w.slots = bal_runs(T) + G;
+    w.p = 0;
+    w.c = align256(w.p + w.slots * E * 4);
+    w.n = align256(w.c + w.slots * E * 4);
+    w.lg = align256(w.n + w.slots * 4);
+    w.ticket = align256(w.lg + G * 4LL);
+    w.bytes = w.ticket + 256;
+    return w;
+}
+
+template <typename T, int EPL>
+static cudaError_t launch_balance(const BalArgs& a, char* ws, const BalWork& w, cudaStream_t st)
+{
+    return launch_free(balance_partial_kernel<T, EPL>, dim3((unsigned)bal_runs(a.T)), dim3(kBalThreads), 0, st,
+                       (const T*)a.logits, a.ldl, a.T, a.E, a.topk, a.K, a.valid, a.cu, a.n_seq,
+                       (float*)(ws + w.p), (int*)(ws + w.c), (int*)(ws + w.n), (int*)(ws + w.ticket));
+}
+
+template <typename T, int EPL>
+static cudaError_t launch_balance_grad(const BalArgs& a, const int32_t* counts, const int32_t* tokens, float scale,
+                                       const float* dr, const float* dl, float* out, cudaStream_t st)
+{
+    return launch_free(balance_grad_kernel<T, EPL>, dim3((unsigned)ceil_div(a.T, kBalThreads / 32)),
+                       dim3(kBalThreads), 0, st, (const T*)a.logits, a.ldl, a.T, a.E, a.topk, a.K, a.valid,
+                       a.cu, a.n_seq, counts, tokens, scale, dr, dl, out);
+}
+
+// Calls FN<T, EPL>(...) for the row width: EPL = logits per lane.
+#define BAL_DISPATCH(FN, ...)                                                                   \
+    with_type(a.dtype, [&](auto z) -> cudaError_t {                                             \
+        using T_ = decltype(z);                                                                 \
+        switch ((a.E + 31) / 32) {                                                              \
+            case 1: return FN<T_, 1>(__VA_ARGS__);                                              \
+            case 2: return FN<T_, 2>(__VA_ARGS__);                                              \
+            case 3: return FN<T_, 3>(__VA_ARGS__);                                              \
+            case 4: return FN<T_, 4>(__VA_ARGS__);                                              \
+            case 5: return FN<T_, 5>(__VA_ARGS__);                                              \
+            case 6: return FN<T_, 6>(__VA_ARGS__);                                              \
+            case 7: return FN<T_, 7>(__VA_ARGS__);                                              \
+            default: return FN<T_, 8>(__VA_ARGS__);                                             \
+        }                                                                                       \
+    })
+
+extern "C" {
+
+int64_t beam_balance_workspace(int32_t T, int32_t E, int32_t n_seq)
+{
+    if (T < 0 || E < 1 || E > kMaxExperts || n_seq < 0 || n_seq > 65536) return -1;
+    return bal_work(T, E, n_seq).bytes;
+}
+
+beam_status_t beam_balance_forward(const void* logits, int32_t dtype, int32_t T, int32_t E,
+                                   int64_t ld_logits, const int32_t* topk_id, int32_t K,
+                                   const uint8_t* valid, const int32_t* cu_seqlens, int32_t n_seq,
+                                   float* loss, float* prob, int32_t* counts, int32_t* tokens,
+                                   void* workspace, int64_t workspace_bytes, void* stream)
+{
+    beam_host_clear_error();
+    const BalArgs a{logits, dtype, T, E, ld_logits, topk_id, K, valid, cu_seqlens, n_seq};
+    TRY(check_balance(a));
+    if (!loss || !prob || !counts || !tokens) FAIL_ARG("an output pointer is NULL");
+    if (misaligned(loss, 4) || misaligned(prob, 4) || misaligned(counts, 4) || misaligned(tokens, 4))
+        FAIL_ARG("the outputs must be 4-byte aligned");
+    const BalWork w = bal_work(T, E, n_seq);
+    if (!workspace || workspace_bytes < w.bytes || misaligned(workspace, 16))
+        FAIL_ARG("the workspace must be 16-byte aligned and hold %lld bytes", w.bytes);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    BEAM_HOST_CUDA(BAL_DISPATCH(launch_balance, a, ws, w, st));
+    BEAM_HOST_CUDA(launch_free(balance_reduce_kernel, dim3((unsigned)std::max(1, n_seq)), dim3(256), 0, st,
+                               (const float*)(ws + w.p), (const int*)(ws + w.c), (const int*)(ws + w.n), T, E, K,
+                               cu_seqlens, (float*)(ws + w.lg), (int*)(ws + w.ticket), prob, counts, tokens, loss));
+    return BEAM_OK;
+}
+
+beam_status_t beam_balance_backward(const void* logits, int32_t dtype, int32_t T, int32_t E,
+                                    int64_t ld_logits, const int32_t* topk_id, int32_t K,
+                                    const uint8_t* valid, const int32_t* cu_seqlens, int32_t n_seq,
+                                    const int32_t* counts, const int32_t* tokens, float scale,
+                                    const float* d_gate_logit, const float* d_mask_logit,
+                                    float* dlogits, void* stream)
+{
+    beam_host_clear_error();
+    const BalArgs a{logits, dtype, T, E, ld_logits, topk_id, K, valid, cu_seqlens, n_seq};
+    TRY(check_balance(a));
+    if (!std::isfinite(scale)) FAIL_ARG("scale must be finite");
+    if (!d_gate_logit != !d_mask_logit) FAIL_ARG("d_gate_logit and d_mask_logit come together");
+    if (T > 0 && (!counts || !tokens || !dlogits)) FAIL_ARG("counts, tokens and dlogits are required");
+    if (misaligned(counts, 4) || misaligned(tokens, 4) || misaligned(dlogits, 4) || misaligned(d_gate_logit, 4) ||
+        misaligned(d_mask_logit, 4))
+        FAIL_ARG("the arrays must be 4-byte aligned");
+    if (T == 0) return BEAM_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    BEAM_HOST_CUDA(BAL_DISPATCH(launch_balance_grad, a, counts, tokens, scale, d_gate_logit, d_mask_logit, dlogits, st));
+    return BEAM_OK;
+}
+
+// ---------------------------------------------------------------- 8-bit checkpoints
+beam_status_t beam_checkpoint_save(const void* x, int32_t dtype, int64_t rows, int32_t d, int64_t ld_x,
+                                   int8_t* q, uint8_t* scale, void* stream)
+{
+    beam_host_clear_error();
+    TRY(check_ckpt(q, scale, rows, d));
+    TRY(check_matrix("x", x, dtype, true, rows, d, ld_x));
+    if (rows == 0) return BEAM_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int nb = (int)ceil_div(d, kCkptBlock);
+    BEAM_HOST_CUDA(with_type3(dtype, [&](auto z) {
+        using T = decltype(z);
+        const unsigned grid = (unsigned)std::min(ceil_div(rows * nb, 8), 148LL * 64);
+        return launch_free(ckpt_save_kernel<T>, dim3(grid), dim3(256), 0, st, (const T*)x, (long long)ld_x,
+                           (long long)rows, d, nb, q, scale);
+    }));
+    return BEAM_OK;
+}
+
+beam_status_t beam_checkpoint_load(const int8_t* q, const uint8_t* scale, int64_t rows, int32_t d, void* y,
+                                   int32_t dtype, void* stream)
+{
+    beam_host_clear_error();
+    TRY(check_ckpt(q, scale, rows, d));
+    TRY(check_matrix("y", y, dtype, true, rows, d, d));
+    if (rows == 0) return BEAM_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int nb = (int)ceil_div(d, kCkptBlock);
+    BEAM_HOST_CUDA(with_type3(dtype, [&](auto z) {
+        using T = decltype(z);
+        const unsigned grid = (unsigned)std::min(ceil_div(rows * nb, 8), 148LL * 64);
+        return launch_free(ckpt_load_kernel<T>, dim3(grid), dim3(256), 0, st, q, scale, (long long)rows, d, nb,
+                           (T*)y);
+    }));
+    return BEAM_OK;
+}
+
+// ---------------------------------------------------------------- slot gradients from a checkpoint
+beam_status_t beam_checkpoint_route_grad(const int8_t* q, const uint8_t* scale, int32_t T, int32_t K, int32_t d,
+                                         const float* gate, const float* mask_logit, const void* dy, int32_t dtype,
+                                         int64_t ld_dy, int32_t segment_len, float reg_scale, float* dghat,
+                                         float* d_gate_logit, float* d_mask_logit, void* stream)
+{
+    beam_host_clear_error();
+    if (T < 0) FAIL_ARG("T=%d is negative", T);
+    if (K < 1 || K > kMaxSlots) FAIL_ARG("K=%d must be in [1, %d]", K, kMaxSlots);
+    TRY(check_ckpt(q, scale, (long long)T * K, d));
+    TRY(check_matrix("dy", dy, dtype, false, T, d, ld_dy));
+    if (segment_len < 0 || segment_len > 65536) FAIL_ARG("segment_len=%d outside [0, 65536]", segment_len);
+    if (!std::isfinite(reg_scale)) FAIL_ARG("reg_scale must be finite");
+    if (T > 0 && (!gate || !mask_logit || !dghat || !d_gate_logit || !d_mask_logit))
+        FAIL_ARG("gate, mask_logit and the outputs are required");
+    if (misaligned(gate, 4) || misaligned(mask_logit, 4) || misaligned(dghat, 4) || misaligned(d_gate_logit, 4) ||
+        misaligned(d_mask_logit, 4))
+        FAIL_ARG("the float32 arrays must be 4-byte aligned");
+    if (T == 0) return BEAM_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int S = std::max(1, segment_len), nb = (int)ceil_div(d, kCkptBlock);
+    const float reg = (float)((double)reg_scale / ((double)T * K));
+    BEAM_HOST_CUDA(with_type(dtype, [&](auto z) {
+        using TY = decltype(z);
+        return launch_free(ckpt_dot_kernel<TY>, dim3((unsigned)ceil_div((long long)T * K, 8)), dim3(256), 0, st, q,
+                           scale, T, K, d, nb, (const TY*)dy, (long long)ld_dy, dghat);
+    }));
+    BEAM_HOST_CUDA(launch_free(ckpt_slot_grad_kernel, dim3((unsigned)ceil_div(ceil_div(T, S), 8)), dim3(256), 0, st,
+                               (const float*)dghat, T, K, S, gate, mask_logit, reg, d_gate_logit, d_mask_logit));
+    return BEAM_OK;
+}
+
+// ---------------------------------------------------------------- the router's linear backward
+static beam_status_t check_linear(int T, int C, int d, const void* g, int dtype, long long ldg)
+{
+    if (T < 0) FAIL_ARG("T=%d is negative", T);
+    if (C < 1 || C > kMaxLogits) FAIL_ARG("C=%d must be in [1, %d]", C, kMaxLogits);
+    if (d < 1 || d > kMaxWidth) FAIL_ARG("d=%d must be in [1, %d]", d, kMaxWidth);
+    return check_matrix("dlogits", g, dtype, false, T, C, ldg);
+}
+
+beam_status_t beam_router_weight_grad(const int8_t* q, const uint8_t* scale, int32_t T, int32_t d,
+                                      const void* dlogits, int32_t dtype, int64_t ld_dlogits, int32_t C,
+                                      int32_t parts, float* dw, void* stream)
+{
+    beam_host_clear_error();
+    TRY(check_linear(T, C, d, dlogits, dtype, ld_dlogits));
+    TRY(check_ckpt(q, scale, T, d));
+    if (parts < 1 || C % parts) FAIL_ARG("parts=%d must divide C=%d", parts, C);
+    if (!dw || misaligned(dw, 4)) FAIL_ARG("dw must be a 4-byte aligned pointer");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int nb = (int)ceil_div(d, kCkptBlock);
+    BEAM_HOST_CUDA(with_type(dtype, [&](auto z) {
+        using TG = decltype(z);
+        return launch_free(router_weight_grad_kernel<TG>,
+                           dim3((unsigned)ceil_div(d, kLinTile), (unsigned)ceil_div(C, kLinTile)), dim3(256), 0, st,
+                           q, scale, T, d, nb, (const TG*)dlogits, (long long)ld_dlogits, C, C / parts, dw);
+    }));
+    return BEAM_OK;
+}
+
+beam_status_t beam_router_input_grad(const void* dlogits, int32_t dtype, int64_t ld_dlogits, int32_t T, int32_t C,
+                                     const void* w, int32_t w_dtype, int64_t ld_w, int32_t d, float* dx,
+                                     void* stream)
+{
+    beam_host_clear_error();
+    TRY(check_linear(T, C, d, dlogits, dtype, ld_dlogits));
+    TRY(check_matrix("w", w, w_dtype, false, d, C, ld_w));
+    if ((T > 0 && !dx) || misaligned(dx, 4)) FAIL_ARG("dx must be a 4-byte aligned pointer");
+    if (T == 0) return BEAM_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    BEAM_HOST_CUDA(with_type(dtype, [&](auto z) {
+        using TG = decltype(z);
+        return with_type(w_dtype, [&](auto zw) {
+            using TW = decltype(zw);
+            return launch_free(router_input_grad_kernel<TG, TW>,
+                               dim3((unsigned)ceil_div(T, kLinTile), (unsigned)ceil_div(d, kLinTile)), dim3(256), 0,
+                               st, (const TG*)dlogits, (long long)ld_dlogits, T, C, (const TW*)w, (long long)ld_w, d,
+                               dx);
+        });
+    }));
+    return BEAM_OK;
+}
+
+}  // extern "C"

@@ -46,7 +46,7 @@ typedef enum {
                                   expert output) overflowed; its y is not valid */
 } beam_status_t;
 
-enum { BEAM_DTYPE_F32 = 0, BEAM_DTYPE_BF16 = 1 };
+enum { BEAM_DTYPE_F32 = 0, BEAM_DTYPE_BF16 = 1, BEAM_DTYPE_F16 = 2 /* checkpoints only */ };
 
 /* forward flags */
 #define BEAM_MASK_OFF     0x1u  /* plain Top-K: every Top-K slot kept (the W_m = 0 behaviour) */
@@ -492,6 +492,105 @@ beam_status_t beam_softtopk_forward(const float *logits_dev, int32_t T, int32_t 
                                     void *stream);
 beam_status_t beam_softtopk_backward(const float *y_dev, const float *dy_dev, int32_t T,
                                      int32_t E, float tau, float *dlogits_dev, void *stream);
+
+/*
+ * ---------------------------------------------------------------- training: balance loss
+ * L_bal of the training objective L = L_lm + alpha L_bal + beta L_reg (BEAM article, training
+ * paragraph).  The article names the term without a formula; the one used is the product of each
+ * expert's share of the assignments and its mean router probability.  The loss is taken over
+ * groups of tokens: the whole batch (cu_seqlens_dev NULL, n_seq 0), or n_seq packed sequences,
+ * sequence g holding the tokens [cu_seqlens[g], cu_seqlens[g + 1]) (device, n_seq + 1 int32,
+ * non-decreasing, within [0, T]).  valid_dev (optional, [T] uint8): a token with 0 is left out, as are the
+ * tokens outside every sequence; their logits may hold anything.  With p_t = softmax(logits_t)
+ * over the E experts (a row of -inf alone has p = 0), n_g the group's tokens and topk_id [T][K]
+ * its assignments (ids outside [0, E) count for no expert):
+ *   counts[g][e] = slots that chose e;   f_ge = counts[g][e] E / (K n_g)
+ *   prob[g][e] = (1 / n_g) sum_t p_te;   tokens[g] = n_g
+ *   loss = mean over the groups with n_g > 0 of sum_e f_ge prob[g][e]   (0 without any)
+ * beam_balance_forward: logits_dev [T][E] of `dtype` (BEAM_DTYPE_F32 or _BF16), rows ld_logits
+ *   elements apart -> loss_dev [1], prob_dev [G][E] float32, counts_dev [G][E] int32, tokens_dev
+ *   [G] int32 (G = n_seq, or 1).  workspace_dev: scratch of at least
+ *   beam_balance_workspace(T, E, n_seq) bytes, 16-byte aligned, free again when the call's
+ *   kernels are done.
+ * beam_balance_backward: the loss's gradient times `scale` for the same inputs and the forward's
+ *   counts and tokens (f is a count and carries no gradient),
+ *   dlogits_tj = scale / (G' n_g) p_tj (f_gj - sum_i f_gi p_ti),  G' = groups with n_g > 0,
+ *   0 for the tokens left out.  Without slot gradients (both NULL) dlogits_dev is [T][E]; with
+ *   d_gate_logit_dev and d_mask_logit_dev [T][K] (beam_moe_backward_router or
+ *   beam_checkpoint_route_grad) it is [T][2E], the whole gradient of the logits x [W_r | W_m]:
+ *   the slots' gate gradients are added to the first E columns at topk_id, the mask gradients
+ *   fill the last E.  topk_id_dev is read only then.
+ * E <= 256, K <= 32, n_seq <= 65536.  Enqueued on `stream` without host synchronisation;
+ * deterministic (fixed order of every float sum).
+ */
+int64_t beam_balance_workspace(int32_t T, int32_t E, int32_t n_seq); /* -1: sizes out of range */
+beam_status_t beam_balance_forward(const void *logits_dev, int32_t dtype, int32_t T, int32_t E,
+                                   int64_t ld_logits, const int32_t *topk_id_dev, int32_t K,
+                                   const uint8_t *valid_dev, const int32_t *cu_seqlens_dev,
+                                   int32_t n_seq, float *loss_dev, float *prob_dev,
+                                   int32_t *counts_dev, int32_t *tokens_dev, void *workspace_dev,
+                                   int64_t workspace_bytes, void *stream);
+beam_status_t beam_balance_backward(const void *logits_dev, int32_t dtype, int32_t T, int32_t E,
+                                    int64_t ld_logits, const int32_t *topk_id_dev, int32_t K,
+                                    const uint8_t *valid_dev, const int32_t *cu_seqlens_dev,
+                                    int32_t n_seq, const int32_t *counts_dev,
+                                    const int32_t *tokens_dev, float scale,
+                                    const float *d_gate_logit_dev, const float *d_mask_logit_dev,
+                                    float *dlogits_dev, void *stream);
+
+/*
+ * ---------------------------------------------------------------- training: 8-bit checkpoints
+ * A checkpoint keeps `rows` rows of d values in one byte each between forward and backward:
+ *   q_dev [rows][d rounded up to 32] int8 (16-byte aligned; the padding holds 0) and
+ *   scale_dev [rows][ceil(d / 32)] uint8, one per block of 32 columns.
+ * A block whose largest magnitude is a has the exponent k = the smallest integer >= -120 with
+ * a <= 127 2^k, the scale byte k + 127 and q = x 2^-k rounded to nearest even; it stands for
+ * q 2^k, off by at most 2^(k-1) (k = 122 limits |q| to 63, so that no value passes float32's
+ * range).  A block with an infinity or a NaN gets the byte 255 and reads back as NaN.
+ * beam_checkpoint_save: x_dev [rows][d], rows ld_x elements apart, float32, bfloat16 or float16.
+ * beam_checkpoint_load: y_dev [rows][d] contiguous, of any of the three types (float16 values
+ *   past 65504 saturate).
+ * d <= 65536.  The callers of q and scale never change them, so one checkpoint serves any
+ * number of backward calls.
+ */
+beam_status_t beam_checkpoint_save(const void *x_dev, int32_t dtype, int64_t rows, int32_t d,
+                                   int64_t ld_x, int8_t *q_dev, uint8_t *scale_dev, void *stream);
+beam_status_t beam_checkpoint_load(const int8_t *q_dev, const uint8_t *scale_dev, int64_t rows,
+                                   int32_t d, void *y_dev, int32_t dtype, void *stream);
+
+/*
+ * The routing's slot gradients (beam_moe_backward_router) from a checkpoint of the expert
+ * outputs: q_dev / scale_dev hold T K rows of d values, row t K + k the output of token t's slot k.
+ * dy_dev [T][d] float32 or bfloat16 (rows ld_dy elements apart); gate_dev and mask_logit_dev
+ * [T][K] float32; segment_len and reg_scale as in the layer.  Writes dghat_dev, d_gate_logit_dev
+ * and d_mask_logit_dev [T][K] float32: dghat = <dy_t, E_k(x_t)>, the other two at each segment's
+ * first token (0 elsewhere).  K <= 32.
+ */
+beam_status_t beam_checkpoint_route_grad(const int8_t *q_dev, const uint8_t *scale_dev, int32_t T,
+                                         int32_t K, int32_t d, const float *gate_dev,
+                                         const float *mask_logit_dev, const void *dy_dev,
+                                         int32_t dtype, int64_t ld_dy, int32_t segment_len,
+                                         float reg_scale, float *dghat_dev,
+                                         float *d_gate_logit_dev, float *d_mask_logit_dev,
+                                         void *stream);
+
+/*
+ * The backward of the router's linear map (logits = x W, W [d][C]) for a dense logit gradient
+ * dlogits_dev [T][C], float32 or bfloat16, rows ld_dlogits elements apart:
+ * beam_router_weight_grad: dW [d][C] float32 = x^T dlogits with x [T][d] from a checkpoint.  With
+ *   parts > 1 (a divisor of C) the columns come as [parts][d][C / parts]: parts = 2 splits
+ *   [W_r | W_m], parts = L the L layers of a mask generator.  T = 0 writes zeros.
+ * beam_router_input_grad: dx_dev [T][d] float32 = dlogits W^T, w_dev [d][C] float32 or bfloat16,
+ *   rows ld_w elements apart.
+ * A dlogits or W value that is not finite makes the outputs it reaches NaN.
+ */
+beam_status_t beam_router_weight_grad(const int8_t *q_dev, const uint8_t *scale_dev, int32_t T,
+                                      int32_t d, const void *dlogits_dev, int32_t dtype,
+                                      int64_t ld_dlogits, int32_t C, int32_t parts, float *dw_dev,
+                                      void *stream);
+beam_status_t beam_router_input_grad(const void *dlogits_dev, int32_t dtype, int64_t ld_dlogits,
+                                     int32_t T, int32_t C, const void *w_dev, int32_t w_dtype,
+                                     int64_t ld_w, int32_t d, float *dx_dev, void *stream);
 
 /* Free every device buffer of the handle (waits for its pending work).  NULL is ignored. */
 void beam_moe_destroy(beam_moe_t *h);
