@@ -38,30 +38,132 @@ __device__ __forceinline__ float ckpt_step(int byte)
 {
     return byte == kCkptNan ? __uint_as_float(0x7fffffffu) : __uint_as_float((uint32_t)byte << 23);
 }
-__device__ __forceinline__ int ckpt_quant(float x, float inv_step, int byte)
+// Four quantised values, one per byte.  Adding 1.5 * 2^23 rounds to an integer (nearest even) and
+// leaves it in the low mantissa bits, in two's complement; x * inv_step is exact, so the fused
+// multiply-add is the one rounding.  (The conversion instruction would run at a quarter of the
+// rate.)  |x * inv_step| <= 127 by the choice of the scale.
+__device__ __forceinline__ uint32_t ckpt_quant4(const float* x, float inv_step, int byte)
 {
-    const int lim = byte == 122 + kCkptBias ? 63 : 127;
-    const int q = __float2int_rn(x * inv_step);   // NaN (a 255 block) converts to 0
-    return max(-lim, min(lim, q));
+    if (byte == kCkptNan) return 0u;
+    constexpr float kRound = 12582912.f;
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float v = x[i];
+        if (byte == 122 + kCkptBias) v = fminf(fmaxf(v, -63.f * ckpt_step(byte)), 63.f * ckpt_step(byte));
+        r[i] = __float_as_uint(fmaf(v, inv_step, kRound));
+    }
+    return __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410);
+}
+// The four integers of a word as floats: byte ^ 0x80 = q + 128 under the exponent of 2^23.
+__device__ __forceinline__ void ckpt_unpack4(uint32_t w, float* f)
+{
+    w ^= 0x80808080u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f[i] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 + i)) - 8388736.f;
 }
 
-// One warp per (row, block), lane = column.
-template <typename T>
-__global__ void __launch_bounds__(256)
+// Position of a unit u of a [rows][per_row] grid, advanced by a fixed step without dividing.
+struct RowPos {
+    long long row;
+    int at, per_row;
+    long long d_row;
+    int d_at;
+    __device__ RowPos(long long u, long long step, int per_row_) : per_row(per_row_)
+    {
+        row = u / per_row; at = (int)(u - row * per_row);
+        d_row = step / per_row; d_at = (int)(step - d_row * per_row);
+    }
+    __device__ void advance()
+    {
+        row += d_row; at += d_at;
+        if (at >= per_row) { at -= per_row; ++row; }
+    }
+};
+
+// Both directions move one 16-byte vector of the wide type per thread and step (V = 4 or 8
+// columns, so 8 or 4 lanes share a block) and V bytes of q: every access of a warp is contiguous.
+// HBM-bound: 2 + 1 + 1/32 bytes per value for a 16-bit type.  kCkptUnroll vectors are in flight
+// per thread.
+constexpr int kCkptThreads = 256, kCkptUnroll = 4;
+
+// x 16-byte aligned with rows a multiple of 16 bytes apart, D a multiple of V.  FLAT: rows
+// contiguous and D a multiple of 32, so that no row index is needed.
+template <typename T, bool FLAT>
+__global__ void __launch_bounds__(kCkptThreads)
 ckpt_save_kernel(const T* __restrict__ x, long long ldx, long long rows, int D, int nb,
                  int8_t* __restrict__ q, uint8_t* __restrict__ scale)
+{
+    constexpr int V = Vec<T>::N, L = kCkptBlock / V;   // L lanes hold a block
+    pdl_wait();
+    const int per_row = nb * L;
+    const long long n = rows * per_row;   // a multiple of L: a block's lanes are in or out together
+    const long long u0 = (long long)blockIdx.x * (kCkptThreads * kCkptUnroll) + threadIdx.x;
+    uint4 raw[kCkptUnroll];
+    RowPos pos(FLAT ? 0 : u0, kCkptThreads, per_row);
+#pragma unroll
+    for (int i = 0; i < kCkptUnroll; ++i) {
+        const long long u = u0 + i * kCkptThreads;
+        raw[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (FLAT) {
+            if (u < n) raw[i] = ldg_stream(x + u * V);
+        } else {
+            if (u < n && pos.at * V < D) raw[i] = ldg_stream(x + pos.row * ldx + pos.at * V);
+            pos.advance();
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kCkptUnroll; ++i) {
+        const long long u = u0 + i * kCkptThreads;
+        float v[V];
+        Vec<T>::widen(raw[i], v);
+        uint32_t a = 0u;
+#pragma unroll
+        for (int j = 0; j < V; ++j) a = max(a, __float_as_uint(v[j]) & 0x7fffffffu);
+#pragma unroll
+        for (int o = 1; o < L; o <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+        const int byte = ckpt_scale_byte(a);
+        const float inv = ckpt_inv_step(byte);
+        if (u < n) {
+            if (V == 8)
+                *reinterpret_cast<uint2*>(q + u * V) =
+                    make_uint2(ckpt_quant4(v, inv, byte), ckpt_quant4(v + V - 4, inv, byte));
+            else
+                *reinterpret_cast<uint32_t*>(q + u * V) = ckpt_quant4(v, inv, byte);
+            if ((threadIdx.x & (L - 1)) == 0) scale[u / L] = (uint8_t)byte;
+        }
+    }
+    pdl_launch_dependents();
+}
+
+// Any row start and stride: a warp takes kCkptUnroll blocks at a time, lane = column.
+template <typename T>
+__global__ void __launch_bounds__(kCkptThreads)
+ckpt_save_any_kernel(const T* __restrict__ x, long long ldx, long long rows, int D, int nb,
+                     int8_t* __restrict__ q, uint8_t* __restrict__ scale)
 {
     pdl_wait();
     const int lane = threadIdx.x & 31;
     const long long n = rows * nb;
-    for (long long b = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); b < n; b += (long long)gridDim.x * 8) {
-        const long long r = b / nb;
-        const int c = (int)(b - r * nb) * kCkptBlock + lane;
-        const float v = c < D ? to_float(x[r * ldx + c]) : 0.f;
-        const uint32_t a = __reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7fffffffu);
+    const long long b0 = ((long long)blockIdx.x * (kCkptThreads / 32) + (threadIdx.x >> 5)) * kCkptUnroll;
+    RowPos pos(b0, 1, nb);
+    float v[kCkptUnroll];
+#pragma unroll
+    for (int i = 0; i < kCkptUnroll; ++i) {
+        const int c = pos.at * kCkptBlock + lane;
+        v[i] = (b0 + i < n && c < D) ? to_float(x[pos.row * ldx + c]) : 0.f;
+        pos.advance();
+    }
+#pragma unroll
+    for (int i = 0; i < kCkptUnroll; ++i) {
+        const uint32_t a = __reduce_max_sync(0xffffffffu, __float_as_uint(v[i]) & 0x7fffffffu);
         const int byte = ckpt_scale_byte(a);
-        q[b * kCkptBlock + lane] = (int8_t)ckpt_quant(v, ckpt_inv_step(byte), byte);
-        if (lane == 0) scale[b] = (uint8_t)byte;
+        const float w[4] = {v[i], 0.f, 0.f, 0.f};
+        if (b0 + i < n) {
+            q[(b0 + i) * kCkptBlock + lane] = (int8_t)ckpt_quant4(w, ckpt_inv_step(byte), byte);
+            if (lane == 0) scale[b0 + i] = (uint8_t)byte;
+        }
     }
     pdl_launch_dependents();
 }
@@ -74,18 +176,80 @@ template <> __device__ __forceinline__ __half ckpt_value<__half>(float v)
     return __float2half_rn(v > 65504.f ? 65504.f : (v < -65504.f ? -65504.f : v));
 }
 
+// V consecutive values of the read-back type in one 16-byte vector.
 template <typename T>
-__global__ void __launch_bounds__(256)
+__device__ __forceinline__ uint4 ckpt_pack(const float* f)
+{
+    constexpr int V = Vec<T>::N;
+    union { T t[V]; uint4 u; } o;
+#pragma unroll
+    for (int j = 0; j < V; ++j) o.t[j] = ckpt_value<T>(f[j]);
+    return o.u;
+}
+
+// y 16-byte aligned, D a multiple of V.  FLAT: D a multiple of 32.
+template <typename T, bool FLAT>
+__global__ void __launch_bounds__(kCkptThreads)
 ckpt_load_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ scale, long long rows,
                  int D, int nb, T* __restrict__ y)
+{
+    constexpr int V = Vec<T>::N, L = kCkptBlock / V;
+    pdl_wait();
+    const int per_row = nb * L;
+    const long long n = rows * per_row;
+    const long long u0 = (long long)blockIdx.x * (kCkptThreads * kCkptUnroll) + threadIdx.x;
+    uint2 raw[kCkptUnroll];
+    int byte[kCkptUnroll];
+#pragma unroll
+    for (int i = 0; i < kCkptUnroll; ++i) {
+        const long long u = u0 + i * kCkptThreads;
+        raw[i] = make_uint2(0u, 0u);
+        byte[i] = kCkptBias;
+        if (u < n) {
+            if (V == 8) raw[i] = __ldg(reinterpret_cast<const uint2*>(q + u * V));
+            else raw[i].x = __ldg(reinterpret_cast<const uint32_t*>(q + u * V));
+            byte[i] = __ldg(scale + u / L);
+        }
+    }
+    RowPos pos(FLAT ? 0 : u0, kCkptThreads, per_row);
+#pragma unroll
+    for (int i = 0; i < kCkptUnroll; ++i) {
+        const long long u = u0 + i * kCkptThreads;
+        float f[8];
+        ckpt_unpack4(raw[i].x, f);
+        if (V == 8) ckpt_unpack4(raw[i].y, f + 4);
+        const float step = ckpt_step(byte[i]);
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] *= step;
+        if (FLAT) {
+            if (u < n) *reinterpret_cast<uint4*>(y + u * V) = ckpt_pack<T>(f);
+        } else {
+            if (u < n && pos.at * V < D) *reinterpret_cast<uint4*>(y + pos.row * D + pos.at * V) = ckpt_pack<T>(f);
+            pos.advance();
+        }
+    }
+    pdl_launch_dependents();
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kCkptThreads)
+ckpt_load_any_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ scale, long long rows,
+                     int D, int nb, T* __restrict__ y)
 {
     pdl_wait();
     const int lane = threadIdx.x & 31;
     const long long n = rows * nb;
-    for (long long b = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); b < n; b += (long long)gridDim.x * 8) {
-        const long long r = b / nb;
-        const int c = (int)(b - r * nb) * kCkptBlock + lane;
-        if (c < D) y[r * D + c] = ckpt_value<T>((float)q[b * kCkptBlock + lane] * ckpt_step(scale[b]));
+    const long long b0 = ((long long)blockIdx.x * (kCkptThreads / 32) + (threadIdx.x >> 5)) * kCkptUnroll;
+    float v[kCkptUnroll];
+#pragma unroll
+    for (int i = 0; i < kCkptUnroll; ++i)
+        v[i] = b0 + i < n ? (float)q[(b0 + i) * kCkptBlock + lane] * ckpt_step(__ldg(scale + b0 + i)) : 0.f;
+    RowPos pos(b0, 1, nb);
+#pragma unroll
+    for (int i = 0; i < kCkptUnroll; ++i) {
+        const int c = pos.at * kCkptBlock + lane;
+        if (b0 + i < n && c < D) y[pos.row * D + c] = ckpt_value<T>(v[i]);
+        pos.advance();
     }
     pdl_launch_dependents();
 }

@@ -5,60 +5,162 @@
 //   dg_k = m_k sum s_tk, m_k = [l_k >= 0];  dmh_k = g_k sum s_tk + n reg
 //   d_l_k = dmh_k sigmoid(l_k)(1 - sigmoid(l_k));  d_r_k = g_k (dg_k - sum_j g_j dg_j)
 // The decision's gradients go to its first token; the others of a segment get 0.
+// HBM-bound: one byte per expert-output value and dy once; at K = 16 the unpacking (a byte permute
+// and an add per value) and the multiply-adds are within a factor of two of the memory time, so
+// nothing else may enter the inner loop.
 #pragma once
 #include "checkpoint.cuh"
 
 namespace beam {
 
-// One warp per (token, slot): the dot product.
-template <typename T>
-__global__ void __launch_bounds__(256)
-ckpt_dot_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ scale, int n_tok, int K,
-                int D, int nb, const T* __restrict__ dy, long long lddy, float* __restrict__ s_out)
+constexpr int kDotThreads = 256, kDotWarps = kDotThreads / 32;
+constexpr int kDotCols = 8 * 32;    // columns of one strip: 8 per lane
+
+// The slot gradients of one decision, lane = slot: run = sum of s over its n tokens.
+__device__ __forceinline__ void slot_grads(bool on, float run, float g, float l, int n, float reg,
+                                           float& gr, float& gl)
 {
-    pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (i < (long long)n_tok * K) {
-        const long long t = i / K;
-        float acc = 0.f;
-        for (int b = 0; b < nb; ++b) {
-            const int c = b * kCkptBlock + lane;
-            if (c < D)
-                acc = fmaf((float)q[(i * nb + b) * kCkptBlock + lane] * ckpt_step(scale[i * nb + b]),
-                           to_float(dy[t * lddy + c]), acc);
+    const float dg = (on && l >= 0.f) ? run : 0.f;
+    const float c = warp_sum(on ? g * dg : 0.f);
+    const float sg = sigmoid_f(l);
+    gr = g * (dg - c);
+    gl = fmaf(run, g, (float)n * reg) * (sg * (1.f - sg));
+}
+
+// Sums v[0..N) over the warp's lanes: afterwards lane k (k < N) holds the total of v[k].  Each
+// step halves the values a lane carries, N - 1 + log2(32 / N) shuffles instead of 5 N.
+template <int N>
+__device__ __forceinline__ float warp_sum_slots(float* v, int lane)
+{
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
         }
-        acc = warp_sum(acc);
-        if (lane == 0) s_out[i] = acc;
+    }
+    float r = v[0];
+#pragma unroll
+    for (int o = N; o < 32; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+    return r;
+}
+
+// Eight columns of a dy row from column c, zeros past D.
+template <typename T>
+__device__ __forceinline__ void load_dy8(const T* __restrict__ row, int c, int D, bool vec, float* f)
+{
+    if (vec && c + 8 <= D) {
+#pragma unroll
+        for (int j = 0; j < 8; j += Vec<T>::N) Vec<T>::widen(ldg_stream(row + c + j), f + j);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = c + j < D ? to_float(row[c + j]) : 0.f;
+    }
+}
+
+// KM: the smallest of 2, 4, 8, 16, 32 that holds K.  WPT warps share a token, each taking every
+// WPT-th strip of its columns for all K slots (dy is read once per token); their sums are added in
+// warp order.  With one-token decisions (grads) the slot gradients follow in the same kernel.
+template <typename T, int KM>
+__global__ void __launch_bounds__(kDotThreads)
+ckpt_dot_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ scale, int n_tok, int K,
+                int D, int nb, const T* __restrict__ dy, long long lddy, int vec, int wpt,
+                const float* __restrict__ gate, const float* __restrict__ mlogit, float reg,
+                int grads, float* __restrict__ s_out, float* __restrict__ d_r, float* __restrict__ d_l)
+{
+    __shared__ float s_part[kDotWarps][32];
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int sub = warp % wpt;
+    const long long t = (long long)blockIdx.x * (kDotWarps / wpt) + warp / wpt;
+    const bool live = t < n_tok;
+    const bool lead = live && sub == 0 && lane < K;
+    const long long o = t * K + lane;
+    float g = 0.f, l = 0.f;
+    if (lead && grads) { g = __ldg(gate + o); l = __ldg(mlogit + o); }
+    float acc[KM];
+#pragma unroll
+    for (int k = 0; k < KM; ++k) acc[k] = 0.f;
+    if (live) {
+        const T* dyr = dy + t * lddy;
+        const int Dp = nb * kCkptBlock;
+        const int8_t* qt = q + t * K * Dp;
+        const uint8_t* st = scale + t * K * nb;
+#pragma unroll 1
+        for (int c = sub * kDotCols + lane * 8; c < Dp; c += wpt * kDotCols) {
+            float f[8];
+            load_dy8(dyr, c, D, vec, f);
+            uint2 w[KM];
+            int byte[KM];
+#pragma unroll
+            for (int k = 0; k < KM; ++k) {
+                if (k < K) {
+                    w[k] = __ldcs(reinterpret_cast<const uint2*>(qt + (long long)k * Dp + c));
+                    byte[k] = __ldg(st + (long long)k * nb + c / kCkptBlock);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < KM; ++k) {
+                if (k < K) {
+                    float v[8], a = 0.f;
+                    ckpt_unpack4(w[k].x, v);
+                    ckpt_unpack4(w[k].y, v + 4);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) a = fmaf(v[j], f[j], a);
+                    acc[k] = fmaf(a, ckpt_step(byte[k]), acc[k]);
+                }
+            }
+        }
+    }
+    float s = warp_sum_slots<KM>(acc, lane);
+    if (wpt > 1) {
+        s_part[warp][lane] = s;
+        __syncthreads();
+        if (sub == 0)
+            for (int i = 1; i < wpt; ++i) s += s_part[warp + i][lane];
+    }
+    if (live && sub == 0) {
+        if (lane < K) s_out[o] = s;
+        if (grads) {
+            float gr, gl;
+            slot_grads(lane < K, s, g, l, 1, reg, gr, gl);
+            if (lane < K) { d_r[o] = gr; d_l[o] = gl; }
+        }
     }
     pdl_launch_dependents();
 }
 
-// One warp per decision, lane = slot.
-__global__ void __launch_bounds__(256)
-ckpt_slot_grad_kernel(const float* __restrict__ s, int n_tok, int K, int S,
+// Segments: a CTA per decision adds the tokens' dots (thread = slot and every 256/KP-th token, KP
+// the power of two that holds K; then the partials in thread order), and zeroes the gradients
+// of the segment's other tokens.
+__global__ void __launch_bounds__(kDotThreads)
+ckpt_slot_grad_kernel(const float* __restrict__ s, int n_tok, int K, int kp, int S,
                       const float* __restrict__ gate, const float* __restrict__ mlogit, float reg,
                       float* __restrict__ d_r, float* __restrict__ d_l)
 {
+    __shared__ float s_part[kDotThreads];
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const long long t0 = r * S, t1 = min((long long)n_tok, t0 + S);
-    if (t0 < n_tok) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    const long long t0 = (long long)blockIdx.x * S, t1 = min((long long)n_tok, t0 + S);
+    const int k = tid & (kp - 1), step = kDotThreads / kp;
+    float run = 0.f;
+    if (k < K)
+#pragma unroll 4
+        for (long long t = t0 + tid / kp; t < t1; t += step) run += __ldg(s + t * K + k);
+    s_part[tid] = run;
+    for (long long i = (t0 + 1) * K + tid; i < t1 * K; i += kDotThreads) { d_r[i] = 0.f; d_l[i] = 0.f; }
+    __syncthreads();
+    if (tid < 32) {
         const bool on = lane < K;
-        float run = 0.f;
-        for (long long t = t0; t < t1; ++t) {
-            if (on) run += s[t * K + lane];
-            if (on && t != t0) { d_r[t * K + lane] = 0.f; d_l[t * K + lane] = 0.f; }
-        }
+        run = 0.f;
+        if (on)
+            for (int i = 0; i < step; ++i) run += s_part[i * kp + lane];
         const float g = on ? gate[t0 * K + lane] : 0.f, l = on ? mlogit[t0 * K + lane] : 0.f;
-        const float dg = (on && l >= 0.f) ? run : 0.f;
-        const float c = warp_sum(g * dg);
-        const float sg = sigmoid_f(l);
-        if (on) {
-            d_r[t0 * K + lane] = g * (dg - c);
-            d_l[t0 * K + lane] = fmaf(run, g, (float)(t1 - t0) * reg) * (sg * (1.f - sg));
-        }
+        float gr, gl;
+        slot_grads(on, run, g, l, (int)(t1 - t0), reg, gr, gl);
+        if (on) { d_r[t0 * K + lane] = gr; d_l[t0 * K + lane] = gl; }
     }
     pdl_launch_dependents();
 }

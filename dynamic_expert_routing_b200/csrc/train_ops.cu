@@ -192,6 +192,25 @@ beam_status_t beam_balance_backward(const void* logits, int32_t dtype, int32_t T
 }
 
 // ---------------------------------------------------------------- 8-bit checkpoints
+}  // extern "C"
+
+// Whether every row splits into whole 16-byte vectors.
+template <typename T>
+static bool vector_rows(const void* x, long long ld, int d)
+{
+    return !misaligned(x, 16) && d % Vec<T>::N == 0 && ld % Vec<T>::N == 0;
+}
+
+// One unit per thread and step: a 16-byte vector (vec), or the lanes of one block each.
+template <typename T>
+static dim3 ckpt_grid(long long rows, int nb, bool vec)
+{
+    const long long threads = rows * nb * (vec ? kCkptBlock / Vec<T>::N : 32);
+    return dim3((unsigned)ceil_div(threads, kCkptThreads * kCkptUnroll));
+}
+
+extern "C" {
+
 beam_status_t beam_checkpoint_save(const void* x, int32_t dtype, int64_t rows, int32_t d, int64_t ld_x,
                                    int8_t* q, uint8_t* scale, void* stream)
 {
@@ -203,9 +222,11 @@ beam_status_t beam_checkpoint_save(const void* x, int32_t dtype, int64_t rows, i
     const int nb = (int)ceil_div(d, kCkptBlock);
     BEAM_HOST_CUDA(with_type3(dtype, [&](auto z) {
         using T = decltype(z);
-        const unsigned grid = (unsigned)std::min(ceil_div(rows * nb, 8), 148LL * 64);
-        return launch_free(ckpt_save_kernel<T>, dim3(grid), dim3(256), 0, st, (const T*)x, (long long)ld_x,
-                           (long long)rows, d, nb, q, scale);
+        auto kernel = ckpt_save_any_kernel<T>;
+        if (vector_rows<T>(x, ld_x, d))
+            kernel = ld_x == d && d % kCkptBlock == 0 ? ckpt_save_kernel<T, true> : ckpt_save_kernel<T, false>;
+        return launch_free(kernel, ckpt_grid<T>(rows, nb, kernel != ckpt_save_any_kernel<T>), dim3(kCkptThreads), 0, st,
+                           (const T*)x, (long long)ld_x, (long long)rows, d, nb, q, scale);
     }));
     return BEAM_OK;
 }
@@ -221,9 +242,10 @@ beam_status_t beam_checkpoint_load(const int8_t* q, const uint8_t* scale, int64_
     const int nb = (int)ceil_div(d, kCkptBlock);
     BEAM_HOST_CUDA(with_type3(dtype, [&](auto z) {
         using T = decltype(z);
-        const unsigned grid = (unsigned)std::min(ceil_div(rows * nb, 8), 148LL * 64);
-        return launch_free(ckpt_load_kernel<T>, dim3(grid), dim3(256), 0, st, q, scale, (long long)rows, d, nb,
-                           (T*)y);
+        auto kernel = ckpt_load_any_kernel<T>;
+        if (vector_rows<T>(y, d, d)) kernel = d % kCkptBlock == 0 ? ckpt_load_kernel<T, true> : ckpt_load_kernel<T, false>;
+        return launch_free(kernel, ckpt_grid<T>(rows, nb, kernel != ckpt_load_any_kernel<T>), dim3(kCkptThreads), 0, st, q,
+                           scale, (long long)rows, d, nb, (T*)y);
     }));
     return BEAM_OK;
 }
@@ -250,13 +272,29 @@ beam_status_t beam_checkpoint_route_grad(const int8_t* q, const uint8_t* scale, 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int S = std::max(1, segment_len), nb = (int)ceil_div(d, kCkptBlock);
     const float reg = (float)((double)reg_scale / ((double)T * K));
+    // warps per token: the fewest that give every SM 16 warps, as long as each has a strip of columns
+    int wpt = 1;
+    while (wpt < kDotWarps && (long long)T * wpt < 148 * 16 && wpt * kDotCols < d) wpt *= 2;
+    const bool grads = S == 1;
     BEAM_HOST_CUDA(with_type(dtype, [&](auto z) {
         using TY = decltype(z);
-        return launch_free(ckpt_dot_kernel<TY>, dim3((unsigned)ceil_div((long long)T * K, 8)), dim3(256), 0, st, q,
-                           scale, T, K, d, nb, (const TY*)dy, (long long)ld_dy, dghat);
+        auto go = [&](auto kernel) {
+            return launch_free(kernel, dim3((unsigned)ceil_div(T, kDotWarps / wpt)), dim3(kDotThreads), 0, st, q, scale, T,
+                               K, d, nb, (const TY*)dy, (long long)ld_dy, (int)(!misaligned(dy, 16) && ld_dy % Vec<TY>::N == 0),
+                               wpt, gate, mask_logit, reg, (int)grads, dghat, d_gate_logit, d_mask_logit);
+        };
+        if (K <= 2) return go(ckpt_dot_kernel<TY, 2>);
+        if (K <= 4) return go(ckpt_dot_kernel<TY, 4>);
+        if (K <= 8) return go(ckpt_dot_kernel<TY, 8>);
+        if (K <= 16) return go(ckpt_dot_kernel<TY, 16>);
+        return go(ckpt_dot_kernel<TY, 32>);
     }));
-    BEAM_HOST_CUDA(launch_free(ckpt_slot_grad_kernel, dim3((unsigned)ceil_div(ceil_div(T, S), 8)), dim3(256), 0, st,
-                               (const float*)dghat, T, K, S, gate, mask_logit, reg, d_gate_logit, d_mask_logit));
+    if (!grads) {
+        int kp = 1;
+        while (kp < K) kp *= 2;
+        BEAM_HOST_CUDA(launch_free(ckpt_slot_grad_kernel, dim3((unsigned)ceil_div(T, S)), dim3(kDotThreads), 0, st,
+                                   (const float*)dghat, T, K, kp, S, gate, mask_logit, reg, d_gate_logit, d_mask_logit));
+    }
     return BEAM_OK;
 }
 

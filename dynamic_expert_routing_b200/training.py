@@ -37,24 +37,27 @@ def _on_stream(fn):
     return call
 
 
-def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+def _stream(device: torch.device) -> int:
+    """The handle of the device's current stream (the raw query: torch.cuda.current_stream()
+    builds a Stream object, 3 us of a call that launches in 5)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _matrix(name: str, t: torch.Tensor, dtypes: dict, device=None) -> int:
-    """A [rows][cols] CUDA tensor whose rows are contiguous; returns its library type."""
+def _matrix(name: str, t: torch.Tensor, dtypes: dict, device=None):
+    """(type, rows, cols, row stride) of a 2-dimensional CUDA tensor with contiguous rows."""
     dt = dtypes.get(t.dtype)
-    if dt is None or not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) \
-            or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
-        raise ValueError(f"{name} must be a 2-dimensional CUDA tensor with contiguous rows, of "
-                         f"dtype {' or '.join(str(d) for d in dtypes)}")
+    if dt is None or not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-dimensional CUDA tensor of dtype "
+                         f"{' or '.join(str(d) for d in dtypes)}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}")
-    return dt
-
-
-def _ld(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    rows, cols = t.shape
+    ld, inner = t.stride()
+    if rows <= 1:
+        ld = cols
+    if (inner != 1 and cols > 1) or ld < cols:
+        raise ValueError(f"{name} must have contiguous, non-overlapping rows")
+    return dt, rows, cols, ld
 
 
 def _array(name: str, t: torch.Tensor, dtype, shape, device) -> int:
@@ -64,20 +67,18 @@ def _array(name: str, t: torch.Tensor, dtype, shape, device) -> int:
     return t.data_ptr()
 
 
-def _groups(logits, topk_id, valid, cu_seqlens):
-    T, E = logits.shape
-    dev = logits.device
+def _groups(T, dev, topk_id, valid, cu_seqlens):
     if topk_id.dim() != 2 or topk_id.shape[0] != T:
         raise ValueError("topk_id must have the shape [T][K]")
     K = topk_id.shape[1]
     ids = _array("topk_id", topk_id, torch.int32, (T, K), dev)
     v = None if valid is None else _array("valid", valid, torch.uint8, (T,), dev)
     if cu_seqlens is None:
-        return T, E, K, ids, v, None, 0
+        return K, ids, v, None, 0
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
         raise ValueError("cu_seqlens must hold the sequences' bounds: n_seq + 1 values")
     n = cu_seqlens.shape[0] - 1
-    return T, E, K, ids, v, _array("cu_seqlens", cu_seqlens, torch.int32, (n + 1,), dev), n
+    return K, ids, v, _array("cu_seqlens", cu_seqlens, torch.int32, (n + 1,), dev), n
 
 
 @_on_stream
@@ -88,19 +89,20 @@ def balance_loss(logits: torch.Tensor, topk_id: torch.Tensor, valid: torch.Tenso
     (cu_seqlens [n_seq + 1] int32), leaving out the tokens with valid [T] uint8 = 0.  Returns
     loss (a float32 scalar tensor), counts [G][E] int32 (slots per expert), prob [G][E] float32
     (mean router probabilities) and tokens [G] int32.  See beam_balance_forward."""
-    dt = _matrix("logits", logits, _DTYPES)
-    T, E, K, ids, v, cu, n = _groups(logits, topk_id, valid, cu_seqlens)
+    dt, T, E, ld = _matrix("logits", logits, _DTYPES)
+    dev = logits.device
+    K, ids, v, cu, n = _groups(T, dev, topk_id, valid, cu_seqlens)
     lib = _lib.load()
-    dev, G = logits.device, max(1, n)
+    G = max(1, n)
     size = lib.beam_balance_workspace(T, E, n)
     loss = torch.empty((), dtype=torch.float32, device=dev)
     prob = torch.empty((G, E), dtype=torch.float32, device=dev)
     counts = torch.empty((G, E), dtype=torch.int32, device=dev)
     tokens = torch.empty((G,), dtype=torch.int32, device=dev)
     ws = torch.empty((max(size, 0),), dtype=torch.uint8, device=dev)
-    check(lib.beam_balance_forward(logits.data_ptr(), dt, T, E, _ld(logits), ids, K, v, cu, n,
+    check(lib.beam_balance_forward(logits.data_ptr(), dt, T, E, ld, ids, K, v, cu, n,
                                    loss.data_ptr(), prob.data_ptr(), counts.data_ptr(),
-                                   tokens.data_ptr(), ws.data_ptr(), size, _stream()))
+                                   tokens.data_ptr(), ws.data_ptr(), size, _stream(dev)))
     return dict(loss=loss, counts=counts, prob=prob, tokens=tokens)
 
 
@@ -115,9 +117,10 @@ def balance_loss_backward(logits: torch.Tensor, topk_id: torch.Tensor, balance: 
     d_mask_logit [T][K] float32 the result is the whole gradient of x [W_r | W_m], [T][2E]: the
     gate gradients added at topk_id, the mask gradients in the last E columns.  See
     beam_balance_backward."""
-    dt = _matrix("logits", logits, _DTYPES)
-    T, E, K, ids, v, cu, n = _groups(logits, topk_id, valid, cu_seqlens)
-    dev, G = logits.device, max(1, n)
+    dt, T, E, ld = _matrix("logits", logits, _DTYPES)
+    dev = logits.device
+    K, ids, v, cu, n = _groups(T, dev, topk_id, valid, cu_seqlens)
+    G = max(1, n)
     counts = _array("balance['counts']", balance["counts"], torch.int32, (G, E), dev)
     tokens = _array("balance['tokens']", balance["tokens"], torch.int32, (G,), dev)
     if (d_gate_logit is None) != (d_mask_logit is None):
@@ -127,8 +130,8 @@ def balance_loss_backward(logits: torch.Tensor, topk_id: torch.Tensor, balance: 
         gr = _array("d_gate_logit", d_gate_logit, torch.float32, (T, K), dev)
         gl = _array("d_mask_logit", d_mask_logit, torch.float32, (T, K), dev)
     out = torch.empty((T, E if gr is None else 2 * E), dtype=torch.float32, device=dev)
-    check(_lib.load().beam_balance_backward(logits.data_ptr(), dt, T, E, _ld(logits), ids, K, v, cu,
-                                            n, counts, tokens, scale, gr, gl, out.data_ptr(), _stream()))
+    check(_lib.load().beam_balance_backward(logits.data_ptr(), dt, T, E, ld, ids, K, v, cu,
+                                            n, counts, tokens, scale, gr, gl, out.data_ptr(), _stream(dev)))
     return out
 
 
@@ -138,13 +141,12 @@ def checkpoint_save(x: torch.Tensor) -> dict:
     dict of q [rows][d rounded up to 32] int8, scale [rows][ceil(d / 32)] uint8 and d.  A block of
     32 columns shares a power-of-two scale: values are kept to within 1/127 of the block's largest.
     Rows may be taken out of q and scale by indexing both alike.  See beam_checkpoint_save."""
-    dt = _matrix("x", x, _CKPT_DTYPES)
-    n, d = x.shape
-    nb = -(-d // CKPT_BLOCK)
-    q = torch.empty((n, nb * CKPT_BLOCK), dtype=torch.int8, device=x.device)
-    scale = torch.empty((n, nb), dtype=torch.uint8, device=x.device)
-    check(_lib.load().beam_checkpoint_save(x.data_ptr(), dt, n, d, _ld(x), q.data_ptr(),
-                                           scale.data_ptr(), _stream()))
+    dt, n, d, ld = _matrix("x", x, _CKPT_DTYPES)
+    dev, nb = x.device, -(-d // CKPT_BLOCK)
+    q = torch.empty((n, nb * CKPT_BLOCK), dtype=torch.int8, device=dev)
+    scale = torch.empty((n, nb), dtype=torch.uint8, device=dev)
+    check(_lib.load().beam_checkpoint_save(x.data_ptr(), dt, n, d, ld, q.data_ptr(),
+                                           scale.data_ptr(), _stream(dev)))
     return dict(q=q, scale=scale, d=d)
 
 
@@ -165,8 +167,9 @@ def checkpoint_load(ckpt: dict, dtype: torch.dtype = torch.float32) -> torch.Ten
     if dt is None:
         raise TypeError(f"unsupported dtype {dtype}")
     q, scale, n, d = _checkpoint(ckpt)
-    y = torch.empty((n, d), dtype=dtype, device=ckpt["q"].device)
-    check(_lib.load().beam_checkpoint_load(q, scale, n, d, y.data_ptr(), dt, _stream()))
+    dev = ckpt["q"].device
+    y = torch.empty((n, d), dtype=dtype, device=dev)
+    check(_lib.load().beam_checkpoint_load(q, scale, n, d, y.data_ptr(), dt, _stream(dev)))
     return y
 
 
@@ -184,14 +187,14 @@ def checkpoint_route_grad(ckpt: dict, gate: torch.Tensor, mask_logit: torch.Tens
     T, K = gate.shape
     g = _array("gate", gate, torch.float32, (T, K), dev)
     l = _array("mask_logit", mask_logit, torch.float32, (T, K), dev)
-    dt = _matrix("dy", dy, _DTYPES, dev)
-    if tuple(dy.shape) != (T, d) or n != T * K:
+    dt, rows, cols, ld = _matrix("dy", dy, _DTYPES, dev)
+    if rows != T or cols != d or n != T * K:
         raise ValueError(f"dy must be [T][d] and the checkpoint hold T*K rows: got dy {tuple(dy.shape)}, "
                          f"{n} rows of {d} values, gate {(T, K)}")
     out = [torch.empty((T, K), dtype=torch.float32, device=dev) for _ in range(3)]
-    check(_lib.load().beam_checkpoint_route_grad(q, scale, T, K, d, g, l, dy.data_ptr(), dt, _ld(dy),
+    check(_lib.load().beam_checkpoint_route_grad(q, scale, T, K, d, g, l, dy.data_ptr(), dt, ld,
                                                  segment_len, reg_scale, out[0].data_ptr(),
-                                                 out[1].data_ptr(), out[2].data_ptr(), _stream()))
+                                                 out[1].data_ptr(), out[2].data_ptr(), _stream(dev)))
     return dict(dghat=out[0], d_gate_logit=out[1], d_mask_logit=out[2])
 
 
@@ -202,15 +205,14 @@ def router_weight_grad(ckpt: dict, dlogits: torch.Tensor, parts: int = 1) -> tor
     [parts][d][C / parts] (2: W_r and W_m; L: a mask generator's layers)."""
     q, scale, n, d = _checkpoint(ckpt)
     dev = ckpt["q"].device
-    dt = _matrix("dlogits", dlogits, _DTYPES, dev)
-    T, C = dlogits.shape
+    dt, T, C, ld = _matrix("dlogits", dlogits, _DTYPES, dev)
     if T != n:
         raise ValueError(f"dlogits has {T} rows, the checkpoint {n}")
     if parts < 1 or C % parts:
         raise ValueError(f"parts={parts} must divide the {C} columns of dlogits")
     dw = torch.empty((d, C) if parts == 1 else (parts, d, C // parts), dtype=torch.float32, device=dev)
-    check(_lib.load().beam_router_weight_grad(q, scale, T, d, dlogits.data_ptr(), dt, _ld(dlogits), C,
-                                              parts, dw.data_ptr(), _stream()))
+    check(_lib.load().beam_router_weight_grad(q, scale, T, d, dlogits.data_ptr(), dt, ld, C,
+                                              parts, dw.data_ptr(), _stream(dev)))
     return dw
 
 
@@ -218,13 +220,12 @@ def router_weight_grad(ckpt: dict, dlogits: torch.Tensor, parts: int = 1) -> tor
 def router_input_grad(dlogits: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
     """dx [T][d] float32 = dlogits W^T of a router logits = x W, for dlogits [T][C] and w [d][C]
     (each float32 or bfloat16; rows may be strided)."""
-    dt = _matrix("dlogits", dlogits, _DTYPES)
-    wt = _matrix("w", w, _DTYPES, dlogits.device)
-    T, C = dlogits.shape
-    if w.shape[1] != C:
+    dt, T, C, ld = _matrix("dlogits", dlogits, _DTYPES)
+    dev = dlogits.device
+    wt, d, cols, lw = _matrix("w", w, _DTYPES, dev)
+    if cols != C:
         raise ValueError(f"w must have dlogits' {C} columns")
-    d = w.shape[0]
-    dx = torch.empty((T, d), dtype=torch.float32, device=dlogits.device)
-    check(_lib.load().beam_router_input_grad(dlogits.data_ptr(), dt, _ld(dlogits), T, C, w.data_ptr(),
-                                             wt, _ld(w), d, dx.data_ptr(), _stream()))
+    dx = torch.empty((T, d), dtype=torch.float32, device=dev)
+    check(_lib.load().beam_router_input_grad(dlogits.data_ptr(), dt, ld, T, C, w.data_ptr(),
+                                             wt, lw, d, dx.data_ptr(), _stream(dev)))
     return dx
