@@ -29,15 +29,13 @@ __device__ __forceinline__ int ckpt_scale_byte(uint32_t a)
     const int e = (int)((a + 0x1ffffu) >> 23);   // biased exponent, carried
     return max(e - 6, kCkptMinExp + kCkptBias);
 }
-// 2^-k and 2^k of a scale byte (both normal floats for k in [-120, 122]); NaN for byte 255.
+// 2^-k of a scale byte (a normal float for k in [-120, 122]), for the blocks that are quantised.
 __device__ __forceinline__ float ckpt_inv_step(int byte)
 {
-    return byte == kCkptNan ? __uint_as_float(0x7fffffffu) : __uint_as_float((uint32_t)(254 - byte) << 23);
+    return __uint_as_float((uint32_t)(254 - byte) << 23);
 }
-__device__ __forceinline__ float ckpt_step(int byte)
-{
-    return byte == kCkptNan ? __uint_as_float(0x7fffffffu) : __uint_as_float((uint32_t)byte << 23);
-}
+// 2^k; an infinity for byte 255, whose block holds q = 0: every product with it is NaN.
+__device__ __forceinline__ float ckpt_step(int byte) { return __uint_as_float((uint32_t)byte << 23); }
 // Four quantised values, one per byte.  Adding 1.5 * 2^23 rounds to an integer (nearest even) and
 // leaves it in the low mantissa bits, in two's complement; x * inv_step is exact, so the fused
 // multiply-add is the one rounding.  (The conversion instruction would run at a quarter of the

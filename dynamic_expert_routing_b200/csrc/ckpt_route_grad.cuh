@@ -14,7 +14,7 @@
 namespace beam {
 
 constexpr int kDotThreads = 256, kDotWarps = kDotThreads / 32;
-constexpr int kDotCols = 8 * 32;    // columns of one strip: 8 per lane
+constexpr int kDotCols = 16 * 32;   // columns of one strip: 16 per lane, one 16-byte load of q
 
 // The slot gradients of one decision, lane = slot: run = sum of s over its n tokens.
 __device__ __forceinline__ void slot_grads(bool on, float run, float g, float l, int n, float reg,
@@ -47,16 +47,17 @@ __device__ __forceinline__ float warp_sum_slots(float* v, int lane)
     return r;
 }
 
-// Eight columns of a dy row from column c, zeros past D.
+// Sixteen columns of a dy row from column c, zeros past D.
 template <typename T>
-__device__ __forceinline__ void load_dy8(const T* __restrict__ row, int c, int D, bool vec, float* f)
+__device__ __forceinline__ void load_dy16(const T* __restrict__ row, int c, int D, bool vec, float* f)
 {
-    if (vec && c + 8 <= D) {
+    if (vec && c + 16 <= D) {
 #pragma unroll
-        for (int j = 0; j < 8; j += Vec<T>::N) Vec<T>::widen(ldg_stream(row + c + j), f + j);
+        for (int j = 0; j < 16; j += Vec<T>::N)
+            Vec<T>::widen(__ldg(reinterpret_cast<const uint4*>(row + c + j)), f + j);
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = c + j < D ? to_float(row[c + j]) : 0.f;
+        for (int j = 0; j < 16; ++j) f[j] = c + j < D ? to_float(row[c + j]) : 0.f;
     }
 }
 
@@ -64,7 +65,7 @@ __device__ __forceinline__ void load_dy8(const T* __restrict__ row, int c, int D
 // WPT-th strip of its columns for all K slots (dy is read once per token); their sums are added in
 // warp order.  With one-token decisions (grads) the slot gradients follow in the same kernel.
 template <typename T, int KM>
-__global__ void __launch_bounds__(kDotThreads)
+__global__ void __launch_bounds__(kDotThreads, KM <= 16 ? 2 : 1)
 ckpt_dot_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ scale, int n_tok, int K,
                 int D, int nb, const T* __restrict__ dy, long long lddy, int vec, int wpt,
                 const float* __restrict__ gate, const float* __restrict__ mlogit, float reg,
@@ -84,32 +85,41 @@ ckpt_dot_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ scale,
 #pragma unroll
     for (int k = 0; k < KM; ++k) acc[k] = 0.f;
     if (live) {
+        constexpr int B = KM < 8 ? KM : 8;   // slots whose loads are in flight together
         const T* dyr = dy + t * lddy;
         const int Dp = nb * kCkptBlock;
         const int8_t* qt = q + t * K * Dp;
         const uint8_t* st = scale + t * K * nb;
 #pragma unroll 1
-        for (int c = sub * kDotCols + lane * 8; c < Dp; c += wpt * kDotCols) {
-            float f[8];
-            load_dy8(dyr, c, D, vec, f);
-            uint2 w[KM];
-            int byte[KM];
+        for (int c = (sub * 32 + lane) * 16; c < Dp; c += wpt * kDotCols) {
+            float f[16];
+            load_dy16(dyr, c, D, vec, f);
+            const int8_t* qc = qt + c;
+            const uint8_t* sc = st + c / kCkptBlock;
 #pragma unroll
-            for (int k = 0; k < KM; ++k) {
-                if (k < K) {
-                    w[k] = __ldcs(reinterpret_cast<const uint2*>(qt + (long long)k * Dp + c));
-                    byte[k] = __ldg(st + (long long)k * nb + c / kCkptBlock);
+            for (int k0 = 0; k0 < KM; k0 += B) {
+                if (k0 >= K) break;
+                uint4 w[B];
+                int byte[B];
+#pragma unroll
+                for (int k = 0; k < B; ++k) {
+                    // slots past K repeat the last one: no branch, and their sums are dropped
+                    const int ks = min(k0 + k, K - 1);
+                    w[k] = __ldcs(reinterpret_cast<const uint4*>(qc + ks * Dp));
+                    byte[k] = __ldg(sc + ks * nb);
                 }
-            }
 #pragma unroll
-            for (int k = 0; k < KM; ++k) {
-                if (k < K) {
-                    float v[8], a = 0.f;
-                    ckpt_unpack4(w[k].x, v);
-                    ckpt_unpack4(w[k].y, v + 4);
+                for (int k = 0; k < B; ++k) {
+                    const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+                    float a0 = 0.f, a1 = 0.f;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) a = fmaf(v[j], f[j], a);
-                    acc[k] = fmaf(a, ckpt_step(byte[k]), acc[k]);
+                    for (int j = 0; j < 4; ++j) {
+                        float v[4];
+                        ckpt_unpack4(u[j], v);
+                        a0 = fmaf(v[0], f[4 * j], a0); a1 = fmaf(v[1], f[4 * j + 1], a1);
+                        a0 = fmaf(v[2], f[4 * j + 2], a0); a1 = fmaf(v[3], f[4 * j + 3], a1);
+                    }
+                    acc[k0 + k] = fmaf(a0 + a1, ckpt_step(byte[k]), acc[k0 + k]);
                 }
             }
         }
