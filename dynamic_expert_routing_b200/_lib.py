@@ -124,7 +124,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.beam_checkpoint_save.argtypes = [P, I, Q, I, Q, P, P, P]
     lib.beam_checkpoint_load.argtypes = [P, P, Q, I, P, I, P]
     lib.beam_checkpoint_route_grad.argtypes = [P, P, I, I, I, P, P, P, I, Q, I, Fl, P, P, P, P]
-    lib.beam_router_weight_grad.argtypes = [P, P, I, I, P, I, Q, I, I, P, P]
+    lib.beam_router_weight_grad_workspace.argtypes = [I, I, I]
+    lib.beam_router_weight_grad_workspace.restype = Q
+    lib.beam_router_weight_grad.argtypes = [P, P, I, I, P, I, Q, I, I, P, P, Q, P]
     lib.beam_router_input_grad.argtypes = [P, I, Q, I, I, P, I, Q, I, P, P]
     for f in (lib.beam_balance_forward, lib.beam_balance_backward, lib.beam_checkpoint_save,
               lib.beam_checkpoint_load, lib.beam_checkpoint_route_grad,

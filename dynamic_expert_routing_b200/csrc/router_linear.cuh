@@ -2,73 +2,471 @@
 //   dW[d][c] = sum_t x[t][d] G[t][c]   with x from an 8-bit checkpoint
 //   dx[t][d] = sum_c G[t][c] W[d][c]
 // for the dense logit gradient G [T][C] (the balance term reaches every expert of every token).
+//
+// Both run on the tensor cores (tcgen05, bf16 operands, fp32 accumulation) and keep float32's
+// precision.  A checkpoint value q 2^k and a bf16 value are bf16 operands as they are.  A float32
+// value is the exact sum of three bf16 numbers cut from its 24 significant bits, 8 at a time (its
+// upper half; the upper half of the rest; the rest), and the product of two operands is taken limb by limb: all
+// pairs (i, j) with i + j at most max(limbs) - 1, the terms left out being below 2^-24 of the
+// product.  The tensor cores add into their accumulator with truncation, an error of one sign that
+// grows with the number of additions: the leading product therefore has an accumulator of
+// its own (the small ones share another), and every kChain steps of 64 the accumulators are
+// drained into float32 sums in registers, rounded to nearest.
+//
+// One kernel computes out[m][n] = sum_k A(m, k) B(n, k) on 128 x 128 tiles, 64 of k per step:
+//   dW: m = d, n = c, k = t: A and B lie in memory with m, n contiguous ("MN-major");
+//   dx: m = t, n = d, k = c: k contiguous ("K-major"; MN-major for a repacked W [C][D]).
+// Either way a tile is a block of rows of up to 128 bytes of bf16, and 8 warps write it into
+// shared memory in the 128-byte-swizzled layout that tcgen05.mma reads, converting on the way
+// (the operands are not bf16 in memory, so TMA could not bring them); the major-ness is a bit of the
+// instruction descriptor.  Each thread loads the next step's piece as it converts this one's.
+// One warp issues the MMAs; 8 warps drain TMEM (two accumulator sets, so that a drain overlaps the
+// next steps) and store.  The grid is persistent; when the tiles are fewer than the SMs, k is cut
+// into slices whose partial tiles lin_reduce_kernel adds in order.
+// Every wait is bounded: when one runs out, the kernel's outputs are set to NaN.
 #pragma once
 #include "checkpoint.cuh"
+#include "tc_ptx.cuh"
 
 namespace beam {
+namespace lin {
 
-constexpr int kLinTile = 64, kLinK = 16;
+constexpr int BM = 128, BN = 128, BK = 64;
+constexpr int kLimbBytes = 128 * BK * 2;      // one limb of one operand's tile
+constexpr int kChain = 4;                     // steps added in the tensor cores' accumulator
+constexpr int kLoadWarps = 8, kEpiWarps = 8;
+constexpr int kThreads = 32 * (kLoadWarps + 1 + kEpiWarps);
+constexpr int kMaxStages = 4;
+constexpr int kSmemLimit = 227 * 1024;
 
-// out[m][n] = sum_k a(m, k) b(n, k) on 64 x 64 tiles, 16 outputs per thread.
-template <typename FA, typename FB, typename FO>
-__device__ __forceinline__ void lin_tile(int m0, int n0, int Kd, FA a, FB b, FO out)
+enum Src { SRC_CKPT = 0, SRC_F32 = 1, SRC_BF16 = 2 };
+__host__ __device__ constexpr int limbs(int src) { return src == SRC_F32 ? 3 : 1; }
+
+template <int SA, int SB> __host__ __device__ constexpr int stage_bytes() { return (limbs(SA) + limbs(SB)) * kLimbBytes; }
+template <int SA, int SB> __host__ __device__ constexpr int stages()
 {
-    __shared__ float sa[kLinK][kLinTile + 1], sb[kLinK][kLinTile + 1];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < Kd; k0 += kLinK) {
-        for (int i = threadIdx.x; i < kLinTile * kLinK; i += 256) {
-            const int r = i & (kLinTile - 1), k = i / kLinTile;
-            sa[k][r] = k0 + k < Kd ? a(m0 + r, k0 + k) : 0.f;
-            sb[k][r] = k0 + k < Kd ? b(n0 + r, k0 + k) : 0.f;
-        }
-        __syncthreads();
+    constexpr int n = (kSmemLimit - 2048) / stage_bytes<SA, SB>();
+    return n < kMaxStages ? n : kMaxStages;
+}
+template <int SA, int SB> __host__ __device__ constexpr int accs() { return limbs(SA) * limbs(SB) > 1 ? 2 : 1; }
+template <int SA, int SB> __host__ __device__ constexpr int smem_bytes()
+{
+    return stages<SA, SB>() * stage_bytes<SA, SB>() + 1024 /* alignment */ + 256 /* barriers */;
+}
+
+struct Operand {
+    const void* p;
+    const uint8_t* scale;   // checkpoint: [rows][ld / 32]
+    long long ld;           // elements between rows
+    int vec;                // rows 16-byte aligned
+};
+
+struct Params {
+    Operand a, b;
+    int M, N, K;
+    int m_tiles, n_tiles, k_steps;
+    int split_steps;        // k steps per unit
+    int units;              // slices * m_tiles * n_tiles
+    // Element (m, n) of slice s is at out + s * slice + ((n / cp) * M + m) * cp + n % cp.
+    float* out;
+    long long slice;
+    int cp;
+};
+
+// ---------------------------------------------------------------- operands
+// Eight consecutive values of a row, as loaded.
+template <int SRC> struct Raw;
+template <> struct Raw<SRC_F32> { uint4 a, b; };
+template <> struct Raw<SRC_BF16> { uint4 a; };
+template <> struct Raw<SRC_CKPT> { uint2 w; int byte; };
+
+__device__ __forceinline__ void raw_zero(Raw<SRC_F32>& r) { r.a = r.b = make_uint4(0u, 0u, 0u, 0u); }
+__device__ __forceinline__ void raw_zero(Raw<SRC_BF16>& r) { r.a = make_uint4(0u, 0u, 0u, 0u); }
+__device__ __forceinline__ void raw_zero(Raw<SRC_CKPT>& r) { r.w = make_uint2(0u, 0u); r.byte = kCkptBias; }
+
+// Columns c .. c + 7 (c a multiple of 8) of a row; zeros from column `cols` on.
+__device__ __forceinline__ void raw_load(Raw<SRC_F32>& r, const Operand& o, long long row, int c, int cols)
+{
+    const float* p = static_cast<const float*>(o.p) + row * o.ld + c;
+    if (o.vec && c + 8 <= cols) {
+        r.a = __ldg(reinterpret_cast<const uint4*>(p));
+        r.b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    } else {
+        const uint32_t* u = reinterpret_cast<const uint32_t*>(p);
+        uint32_t v[8];
 #pragma unroll
-        for (int k = 0; k < kLinK; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][ty + 16 * i], sb[k][tx + 16 * j], acc[i][j]);
-        __syncthreads();
+        for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? __ldg(u + j) : 0u;
+        r.a = make_uint4(v[0], v[1], v[2], v[3]);
+        r.b = make_uint4(v[4], v[5], v[6], v[7]);
     }
+}
+__device__ __forceinline__ void raw_load(Raw<SRC_BF16>& r, const Operand& o, long long row, int c, int cols)
+{
+    const unsigned short* p = static_cast<const unsigned short*>(o.p) + row * o.ld + c;
+    if (o.vec && c + 8 <= cols) {
+        r.a = __ldg(reinterpret_cast<const uint4*>(p));
+    } else {
+        uint32_t v[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) out(m0 + ty + 16 * i, n0 + tx + 16 * j, acc[i][j]);
+        for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? __ldg(p + j) : 0u;
+        r.a = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    }
+}
+// Checkpoint rows are padded with zeros to whole blocks, so no column past `cols` needs a test.
+__device__ __forceinline__ void raw_load(Raw<SRC_CKPT>& r, const Operand& o, long long row, int c, int)
+{
+    r.w = __ldg(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(o.p) + row * o.ld + c));
+    r.byte = __ldg(o.scale + row * (o.ld / kCkptBlock) + c / kCkptBlock);
 }
 
-// dW: m = d, n = c, k = t.  dw is [parts][D][C / parts].
-template <typename T>
-__global__ void __launch_bounds__(256)
-router_weight_grad_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ scale,
-                          int n_tok, int D, int nb, const T* __restrict__ g, long long ldg, int C,
-                          int cp, float* __restrict__ dw)
+// The upper halves of two words.
+__device__ __forceinline__ uint32_t pack_hi(uint32_t lo, uint32_t hi) { return __byte_perm(lo, hi, 0x7632); }
+
+// bf16 limbs of the eight values, most significant first.
+__device__ __forceinline__ void raw_limbs(const Raw<SRC_BF16>& r, uint4* o) { o[0] = r.a; }
+__device__ __forceinline__ void raw_limbs(const Raw<SRC_CKPT>& r, uint4* o)
 {
+    float f[8];
+    ckpt_unpack4(r.w.x, f);
+    ckpt_unpack4(r.w.y, f + 4);
+    const float step = ckpt_step(r.byte);
+    uint32_t u[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(f[j] * step);   // exact in bf16
+    o[0] = make_uint4(pack_hi(u[0], u[1]), pack_hi(u[2], u[3]), pack_hi(u[4], u[5]), pack_hi(u[6], u[7]));
+}
+__device__ __forceinline__ void raw_limbs(const Raw<SRC_F32>& r, uint4* o)
+{
+    const uint32_t x[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+    uint32_t mid[8], low[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float rest = __uint_as_float(x[j]) - __uint_as_float(x[j] & 0xffff0000u);   // exact
+        mid[j] = __float_as_uint(rest);
+        low[j] = __float_as_uint(rest - __uint_as_float(mid[j] & 0xffff0000u));           // exact, 8 bits
+    }
+    o[0] = make_uint4(pack_hi(x[0], x[1]), pack_hi(x[2], x[3]), pack_hi(x[4], x[5]), pack_hi(x[6], x[7]));
+    o[1] = make_uint4(pack_hi(mid[0], mid[1]), pack_hi(mid[2], mid[3]), pack_hi(mid[4], mid[5]), pack_hi(mid[6], mid[7]));
+    o[2] = make_uint4(pack_hi(low[0], low[1]), pack_hi(low[2], low[3]), pack_hi(low[4], low[5]), pack_hi(low[6], low[7]));
+}
+
+// ---------------------------------------------------------------- units and steps
+struct Unit { int m0, n0, nt, slice, s0, s1; };
+
+__device__ __forceinline__ bool get_unit(const Params& p, int u, Unit& t)
+{
+    if (u >= p.units) return false;
+    const int nt = u % p.n_tiles, r = u / p.n_tiles;
+    t.n0 = nt * BN;
+    t.m0 = (r % p.m_tiles) * BM;
+    t.slice = r / p.m_tiles;
+    t.s0 = t.slice * p.split_steps;
+    t.s1 = min(p.k_steps, t.s0 + p.split_steps);
+    t.nt = min(BN, (p.N - t.n0 + 63) & ~63);
+    return true;
+}
+
+// The piece i (0..3) of a tile that loader thread `tid` handles: row and 8-column chunk of the
+// tile's block of rows.  MN-major: 64 rows (k) x 16 chunks (two 64-wide blocks); K-major: 128 rows x
+// 8 chunks.  A quarter warp stores 8 different chunks of one row: no bank conflict.
+template <bool MN> struct Piece {
+    int row, chunk;
+    __device__ Piece(int tid, int i)
+    {
+        if (MN) { chunk = tid & 15; row = (tid >> 4) + 16 * i; }
+        else { chunk = tid & 7; row = (tid >> 3) + 32 * i; }
+    }
+    __device__ uint32_t offset() const
+    {
+        return (MN ? (chunk >> 3) * (BK * 128) : 0) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+    }
+};
+
+// One operand of one step: x0 = first m or n of the tile, xs its limit (past it nothing is read:
+// those outputs are never stored), xw the tile's width, k0 the first k.
+template <int SRC, bool MN>
+__device__ __forceinline__ void piece_load(Raw<SRC>& r, const Operand& o, const Piece<MN>& p, int x0, int xs,
+                                           int k0, int K)
+{
+    if (MN) {
+        const int k = k0 + p.row, x = x0 + 8 * p.chunk;
+        if (k < K && x < xs) raw_load(r, o, k, x, xs);
+        else raw_zero(r);
+    } else {
+        const int k = k0 + 8 * p.chunk, x = x0 + p.row;
+        if (k < K && x < xs) raw_load(r, o, x, k, K);
+        else raw_zero(r);
+    }
+}
+
+template <int SRC, bool MN>
+__device__ __forceinline__ void piece_store(const Raw<SRC>& r, uint8_t* tile, const Piece<MN>& p)
+{
+    uint4 l[limbs(SRC)];
+    raw_limbs(r, l);
+#pragma unroll
+    for (int i = 0; i < limbs(SRC); ++i) *reinterpret_cast<uint4*>(tile + i * kLimbBytes + p.offset()) = l[i];
+}
+
+// Shared-memory descriptor of an MN-major tile: blocks of 64 values (128 bytes) of m or n, 64 rows of k
+// each (leading byte offset: the next block), groups of 8 rows 1024 bytes apart.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr)
+{
+    return tc::sw128_desc(saddr) - ((uint64_t)1 << 16) + ((uint64_t)((BK * 128) >> 4) << 16);
+}
+
+// 32 bytes in one store (a whole sector) where the address allows, else one value at a time.
+__device__ __forceinline__ void store8(float* p, const float* v, int n)
+{
+    if (n >= 8 && (reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+        asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                     "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]) : "memory");
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < n) p[j] = v[j];
+    }
+}
+
+template <int SA, bool MNA, int SB, bool MNB>
+__global__ void __launch_bounds__(kThreads, 1)
+lin_gemm_kernel(const __grid_constant__ Params p)
+{
+    constexpr int LA = limbs(SA), LB = limbs(SB), ST = stages<SA, SB>(), ACC = accs<SA, SB>();
+    constexpr int kTmemCols = 2 * ACC * BN;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = tc::smem_u32(smem_raw);
+    const uint32_t base = (raw_addr + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - raw_addr);
+    const uint32_t bars = base + ST * stage_bytes<SA, SB>();
+    auto full_bar = [&](int s) { return bars + 8u * s; };
+    auto empty_bar = [&](int s) { return bars + 8u * (ST + s); };
+    auto tfull_bar = [&](int a) { return bars + 8u * (2 * ST + a); };
+    auto tempty_bar = [&](int a) { return bars + 8u * (2 * ST + 2 + a); };
+    const uint32_t drain_bar = bars + 8u * (2 * ST + 4);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + ST * stage_bytes<SA, SB>() + 8 * (2 * ST + 5));
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < ST; ++s) { tc::mbar_init(full_bar(s), kLoadWarps); tc::mbar_init(empty_bar(s), 1); }
+        for (int a = 0; a < 2; ++a) { tc::mbar_init(tfull_bar(a), 1); tc::mbar_init(tempty_bar(a), kEpiWarps); }
+        tc::mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == kLoadWarps) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(tc::smem_u32(tmem_slot)), "r"(kTmemCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
     pdl_wait();
-    lin_tile(blockIdx.x * kLinTile, blockIdx.y * kLinTile, n_tok,
-        [&](int d, int t) {
-            return d < D ? (float)q[((long long)t * nb) * kCkptBlock + d] *
-                           ckpt_step(scale[(long long)t * nb + d / kCkptBlock]) : 0.f;
-        },
-        [&](int c, int t) { return c < C ? to_float(g[t * ldg + c]) : 0.f; },
-        [&](int d, int c, float v) {
-            if (d < D && c < C) dw[((long long)(c / cp) * D + d) * cp + c % cp] = v;
-        });
+
+    if (warp < kLoadWarps) {
+        // ------------------------------------------------ loaders: global -> bf16 limbs -> shared
+        const int tid = threadIdx.x;
+        Raw<SA> ra[4];
+        Raw<SB> rb[4];
+        Unit t;
+        int u = blockIdx.x, step = 0;
+        bool has = get_unit(p, u, t);
+        if (has) {
+            step = t.s0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                piece_load<SA, MNA>(ra[i], p.a, Piece<MNA>(tid, i), t.m0, p.M, step * BK, p.K);
+                piece_load<SB, MNB>(rb[i], p.b, Piece<MNB>(tid, i), t.n0, p.N, step * BK, p.K);
+            }
+        }
+        int s = 0;
+        uint32_t ph = 0;
+        while (has) {
+            // the step after this one
+            if (++step >= t.s1) {
+                u += gridDim.x;
+                has = get_unit(p, u, t);
+                if (has) step = t.s0;
+            }
+            if (!tc::mbar_wait(empty_bar(s), ph ^ 1u, abort_flag)) break;
+            uint8_t* sa = gbase + s * stage_bytes<SA, SB>();
+            uint8_t* sb = sa + LA * kLimbBytes;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const Piece<MNA> pa(tid, i);
+                const Piece<MNB> pb(tid, i);
+                const Raw<SA> ca = ra[i];
+                const Raw<SB> cb = rb[i];
+                if (has) {
+                    piece_load<SA, MNA>(ra[i], p.a, pa, t.m0, p.M, step * BK, p.K);
+                    piece_load<SB, MNB>(rb[i], p.b, pb, t.n0, p.N, step * BK, p.K);
+                }
+                piece_store<SA, MNA>(ca, sa, pa);
+                piece_store<SB, MNB>(cb, sb, pb);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(full_bar(s));
+            if (++s == ST) { s = 0; ph ^= 1u; }
+        }
+    } else if (warp == kLoadWarps) {
+        if (lane == 0) {
+            // -------------------------------------------- MMA issuer
+            int s = 0, buf = 0;
+            uint32_t ph = 0, bph = 0;
+            bool ok = true, issued = false;
+            Unit t;
+            for (int u = blockIdx.x; ok && get_unit(p, u, t); u += gridDim.x) {
+                const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((MNA ? 1u : 0u) << 15) |
+                                       ((MNB ? 1u : 0u) << 16) | ((uint32_t)(t.nt >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+                for (int step = t.s0; step < t.s1; ++step) {
+                    const int at = (step - t.s0) % kChain;
+                    const uint32_t d0 = tmem_base + (uint32_t)(buf * ACC * BN);
+                    if (at == 0) {
+                        if (!tc::mbar_wait(tempty_bar(buf), bph ^ 1u, abort_flag)) { ok = false; break; }
+                    }
+                    if (!tc::mbar_wait(full_bar(s), ph, abort_flag)) { ok = false; break; }
+                    tc::tc_fence_after();
+                    const uint32_t sa = base + s * stage_bytes<SA, SB>(), sb = sa + LA * kLimbBytes;
+                    const int n16 = (min(BK, p.K - step * BK) + 15) / 16;
+                    for (int kk = 0; kk < n16; ++kk) {
+                        const bool first = at == 0 && kk == 0;
+                        bool first_low = first;
+#pragma unroll
+                        for (int i = 0; i < LA; ++i)
+#pragma unroll
+                            for (int j = 0; j < LB; ++j) {
+                                if (i + j >= (LA > LB ? LA : LB)) continue;
+                                // 16 of k: 32 bytes of a K-major row, 16 rows of an MN-major block
+                                const uint64_t ad = MNA ? mn_desc(sa + i * kLimbBytes + kk * 2048)
+                                                        : tc::sw128_desc(sa + i * kLimbBytes) + 2ull * kk;
+                                const uint64_t bd = MNB ? mn_desc(sb + j * kLimbBytes + kk * 2048)
+                                                        : tc::sw128_desc(sb + j * kLimbBytes) + 2ull * kk;
+                                if (i + j == 0) {
+                                    tc::tc_mma_f16(d0, ad, bd, idesc, first ? 0u : 1u);
+                                } else {
+                                    tc::tc_mma_f16(d0 + BN, ad, bd, idesc, first_low ? 0u : 1u);
+                                    first_low = false;
+                                }
+                            }
+                    }
+                    issued = true;
+                    tc::tc_commit(empty_bar(s));
+                    if (++s == ST) { s = 0; ph ^= 1u; }
+                    if (at == kChain - 1 || step + 1 == t.s1) {
+                        tc::tc_commit(tfull_bar(buf));
+                        if (++buf == 2) { buf = 0; bph ^= 1u; }
+                    }
+                }
+            }
+            if (!ok && issued) {
+                tc::tc_commit(drain_bar);   // completes when every MMA issued so far has finished
+                const unsigned long long t0 = tc::globaltimer();
+                while (!tc::mbar_try_wait(drain_bar, 0) && tc::globaltimer() - t0 < tc::kWaitLimitNs) {}
+            }
+        }
+    } else {
+        // ------------------------------------------------ epilogue: TMEM -> float32 sums -> global
+        const int lb = 32 * (warp & 3);                    // TMEM lanes this warp may access
+        const int half = (warp - kLoadWarps - 1) / 4;      // which 64 columns
+        int buf = 0;
+        uint32_t bph = 0;
+        bool ok = true;
+        Unit t;
+        for (int u = blockIdx.x; get_unit(p, u, t); u += gridDim.x) {
+            float sum[BN / 2];
+#pragma unroll
+            for (int j = 0; j < BN / 2; ++j) sum[j] = 0.f;
+            const bool mine = 64 * half < t.nt;            // a 64-wide tile leaves the other half idle
+            for (int c = t.s0; c < t.s1; c += kChain) {
+                if (ok) ok = tc::mbar_wait(tfull_bar(buf), bph, abort_flag);
+                if (!ok) break;
+                tc::tc_fence_after();
+                if (mine) {
+                    const uint32_t d0 = tmem_base + ((uint32_t)lb << 16) + (uint32_t)(buf * ACC * BN + 64 * half);
+#pragma unroll
+                    for (int a = ACC - 1; a >= 0; --a)     // the small products first
+#pragma unroll
+                        for (int h = 0; h < BN / 2; h += 16) {   // 16 at a time: 64 sums stay in registers
+                            float v[16];
+                            tc::tmem_ld16(d0 + a * BN + h, v);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) sum[h + j] += v[j];
+                        }
+                }
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(tempty_bar(buf));
+                if (++buf == 2) { buf = 0; bph ^= 1u; }
+            }
+            const int m = t.m0 + lb + lane, n0 = t.n0 + 64 * half;
+            if (mine && m < p.M) {
+                float* out = p.out + t.slice * p.slice;
+#pragma unroll
+                for (int j = 0; j < BN / 2; j += 8) {
+                    const int n = n0 + j;
+                    if (n < p.N) {
+                        if (!ok)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) sum[j + i] = __uint_as_float(0x7fffffffu);
+                        const int part = n / p.cp, at = n - part * p.cp;
+                        if (at + 8 <= p.cp || part == (p.N - 1) / p.cp) {
+                            store8(out + ((long long)part * p.M + m) * p.cp + at, sum + j, min(8, p.N - n));
+                        } else {   // the eight columns belong to more than one part
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (n + i < p.N)
+                                    out[((long long)((n + i) / p.cp) * p.M + m) * p.cp + (n + i) % p.cp] = sum[j + i];
+                        }
+                    }
+                }
+            }
+        }
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == kLoadWarps) {
+        __syncwarp();
+        tc::tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
+    }
     pdl_launch_dependents();
 }
 
-// dx: m = t, n = d, k = c.
-template <typename T, typename TW>
+// dw = the slices' partial tiles [slices][M][ld], added in slice order.
 __global__ void __launch_bounds__(256)
-router_input_grad_kernel(const T* __restrict__ g, long long ldg, int n_tok, int C,
-                         const TW* __restrict__ w, long long ldw, int D, float* __restrict__ dx)
+lin_reduce_kernel(const float* __restrict__ part, int slices, long long slice, int M, int N, int ld, int cp,
+                  float* __restrict__ out)
 {
     pdl_wait();
-    lin_tile(blockIdx.x * kLinTile, blockIdx.y * kLinTile, C,
-        [&](int t, int c) { return t < n_tok ? to_float(g[t * ldg + c]) : 0.f; },
-        [&](int d, int c) { return d < D ? to_float(w[d * ldw + c]) : 0.f; },
-        [&](int t, int d, float v) { if (t < n_tok && d < D) dx[(long long)t * D + d] = v; });
+    const int n4 = (N + 3) / 4;
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const int m = (int)(i / n4), n = (int)(i - (long long)m * n4) * 4;
+    if (m < M) {
+        const float4* src = reinterpret_cast<const float4*>(part + (long long)m * ld + n);
+        float4 s = __ldcg(src);
+#pragma unroll 4
+        for (int k = 1; k < slices; ++k) {
+            const float4 v = __ldcg(src + k * (slice >> 2));
+            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+        }
+        const float r[4] = {s.x, s.y, s.z, s.w};
+        const int p0 = n / cp, at = n - p0 * cp;
+        float* dst = out + ((long long)p0 * M + m) * cp + at;
+        if (at + 4 <= cp && n + 4 <= N && (reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
+            *reinterpret_cast<float4*>(dst) = s;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n + j < N) out[((long long)((n + j) / cp) * M + m) * cp + (n + j) % cp] = r[j];
+        }
+    }
     pdl_launch_dependents();
 }
 
+}  // namespace lin
 }  // namespace beam

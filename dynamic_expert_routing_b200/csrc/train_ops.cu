@@ -3,6 +3,7 @@
 // linear backward.  Every call enqueues its kernels on the given stream and allocates nothing;
 // scratch comes from the caller.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 
@@ -299,17 +300,101 @@ beam_status_t beam_checkpoint_route_grad(const int8_t* q, const uint8_t* scale, 
 }
 
 // ---------------------------------------------------------------- the router's linear backward
+}  // extern "C"
+
+static int num_sms()
+{
+    static std::atomic<int> cached[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+    n = cached[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
+        cached[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+// Slices of k: as many as fill the SMs, each of at least kChain steps.
+static void plan_slices(lin::Params& p, int sms)
+{
+    const long long tiles = (long long)p.m_tiles * p.n_tiles;
+    const long long most = std::max(1LL, ceil_div(p.k_steps, lin::kChain));
+    const long long want = std::min(most, std::max(1LL, sms / tiles));
+    p.split_steps = (int)ceil_div(p.k_steps, want);
+    p.units = (int)(tiles * ceil_div(p.k_steps, p.split_steps));
+}
+
+static lin::Params lin_params(int M, int N, int K)
+{
+    lin::Params p = {};
+    p.M = M; p.N = N; p.K = K;
+    p.m_tiles = (int)ceil_div(M, lin::BM);
+    p.n_tiles = (int)ceil_div(N, lin::BN);
+    p.k_steps = (int)ceil_div(K, lin::BK);
+    p.split_steps = p.k_steps;
+    p.units = p.m_tiles * p.n_tiles;
+    return p;
+}
+
+static lin::Operand operand(const void* x, int dtype, long long ld)
+{
+    return {x, nullptr, ld, !misaligned(x, 16) && ld % (16 / elem_size(dtype)) == 0};
+}
+
+template <int SA, bool MNA, int SB, bool MNB>
+static cudaError_t launch_lin(const lin::Params& p, int sms, cudaStream_t st)
+{
+    auto kernel = lin::lin_gemm_kernel<SA, MNA, SB, MNB>;
+    constexpr int smem = lin::smem_bytes<SA, SB>();
+    static std::atomic<unsigned long long> ready;   // devices whose attribute is set
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(1ULL << dev, std::memory_order_relaxed);
+    }
+    return launch_free(kernel, dim3((unsigned)std::min(p.units, sms)), dim3(lin::kThreads), smem, st, p);
+}
+
+// Workspace of the weight gradient: the slices' partial tiles.
+static int weight_ld(int C) { return (C + 7) & ~7; }
+static lin::Params weight_params(int T, int C, int d)
+{
+    lin::Params p = lin_params(d, C, T);
+    plan_slices(p, num_sms());
+    return p;
+}
+static long long weight_bytes(const lin::Params& p)
+{
+    const long long slices = p.units / ((long long)p.m_tiles * p.n_tiles);
+    return slices > 1 ? slices * p.M * weight_ld(p.N) * 4 : 0;
+}
+
 static beam_status_t check_linear(int T, int C, int d, const void* g, int dtype, long long ldg)
 {
     if (T < 0) FAIL_ARG("T=%d is negative", T);
     if (C < 1 || C > kMaxLogits) FAIL_ARG("C=%d must be in [1, %d]", C, kMaxLogits);
     if (d < 1 || d > kMaxWidth) FAIL_ARG("d=%d must be in [1, %d]", d, kMaxWidth);
+    if (ceil_div(T, lin::BM) * ceil_div(d, lin::BN) > (1LL << 30))
+        FAIL_ARG("T=%d rows of %d values are too many", T, d);
     return check_matrix("dlogits", g, dtype, false, T, C, ldg);
+}
+
+extern "C" {
+
+int64_t beam_router_weight_grad_workspace(int32_t T, int32_t d, int32_t C)
+{
+    if (T < 0 || d < 1 || d > kMaxWidth || C < 1 || C > kMaxLogits) return -1;
+    return T == 0 ? 0 : weight_bytes(weight_params(T, C, d));
 }
 
 beam_status_t beam_router_weight_grad(const int8_t* q, const uint8_t* scale, int32_t T, int32_t d,
                                       const void* dlogits, int32_t dtype, int64_t ld_dlogits, int32_t C,
-                                      int32_t parts, float* dw, void* stream)
+                                      int32_t parts, float* dw, void* workspace, int64_t workspace_bytes,
+                                      void* stream)
 {
     beam_host_clear_error();
     TRY(check_linear(T, C, d, dlogits, dtype, ld_dlogits));
@@ -317,13 +402,29 @@ beam_status_t beam_router_weight_grad(const int8_t* q, const uint8_t* scale, int
     if (parts < 1 || C % parts) FAIL_ARG("parts=%d must divide C=%d", parts, C);
     if (!dw || misaligned(dw, 4)) FAIL_ARG("dw must be a 4-byte aligned pointer");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int nb = (int)ceil_div(d, kCkptBlock);
-    BEAM_HOST_CUDA(with_type(dtype, [&](auto z) {
-        using TG = decltype(z);
-        return launch_free(router_weight_grad_kernel<TG>,
-                           dim3((unsigned)ceil_div(d, kLinTile), (unsigned)ceil_div(C, kLinTile)), dim3(256), 0, st,
-                           q, scale, T, d, nb, (const TG*)dlogits, (long long)ld_dlogits, C, C / parts, dw);
-    }));
+    if (T == 0) {
+        BEAM_HOST_CUDA(cudaMemsetAsync(dw, 0, (size_t)d * C * 4, st));
+        return BEAM_OK;
+    }
+    lin::Params p = weight_params(T, C, d);
+    const long long need = weight_bytes(p);
+    if (need > 0 && (!workspace || workspace_bytes < need || misaligned(workspace, 16)))
+        FAIL_ARG("the workspace must be 16-byte aligned and hold %lld bytes", need);
+    p.a = {q, scale, ceil_div(d, kCkptBlock) * kCkptBlock, 1};
+    p.b = operand(dlogits, dtype, ld_dlogits);
+    const int ldp = weight_ld(C), cp = C / parts;
+    p.out = need ? static_cast<float*>(workspace) : dw;
+    p.slice = (long long)d * ldp;
+    p.cp = need ? ldp : cp;
+    const int sms = num_sms();
+    const cudaError_t e = dtype == BEAM_DTYPE_F32 ? launch_lin<lin::SRC_CKPT, true, lin::SRC_F32, true>(p, sms, st)
+                                                  : launch_lin<lin::SRC_CKPT, true, lin::SRC_BF16, true>(p, sms, st);
+    BEAM_HOST_CUDA(e);
+    if (need) {
+        const long long n = (long long)d * ceil_div(C, 4);
+        BEAM_HOST_CUDA(launch_free(lin::lin_reduce_kernel, dim3((unsigned)ceil_div(n, 256)), dim3(256), 0, st,
+                                   (const float*)p.out, (int)(need / (p.slice * 4)), p.slice, d, C, ldp, cp, dw));
+    }
     return BEAM_OK;
 }
 
@@ -337,16 +438,19 @@ beam_status_t beam_router_input_grad(const void* dlogits, int32_t dtype, int64_t
     if ((T > 0 && !dx) || misaligned(dx, 4)) FAIL_ARG("dx must be a 4-byte aligned pointer");
     if (T == 0) return BEAM_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    BEAM_HOST_CUDA(with_type(dtype, [&](auto z) {
-        using TG = decltype(z);
-        return with_type(w_dtype, [&](auto zw) {
-            using TW = decltype(zw);
-            return launch_free(router_input_grad_kernel<TG, TW>,
-                               dim3((unsigned)ceil_div(T, kLinTile), (unsigned)ceil_div(d, kLinTile)), dim3(256), 0,
-                               st, (const TG*)dlogits, (long long)ld_dlogits, T, C, (const TW*)w, (long long)ld_w, d,
-                               dx);
-        });
-    }));
+    lin::Params p = lin_params(T, d, C);
+    p.a = operand(dlogits, dtype, ld_dlogits);
+    p.b = operand(w, w_dtype, ld_w);
+    p.out = dx;
+    p.cp = d;
+    const int sms = num_sms();
+    const bool g32 = dtype == BEAM_DTYPE_F32, w32 = w_dtype == BEAM_DTYPE_F32;
+    const cudaError_t e =
+        g32 ? (w32 ? launch_lin<lin::SRC_F32, false, lin::SRC_F32, false>(p, sms, st)
+                   : launch_lin<lin::SRC_F32, false, lin::SRC_BF16, false>(p, sms, st))
+            : (w32 ? launch_lin<lin::SRC_BF16, false, lin::SRC_F32, false>(p, sms, st)
+                   : launch_lin<lin::SRC_BF16, false, lin::SRC_BF16, false>(p, sms, st));
+    BEAM_HOST_CUDA(e);
     return BEAM_OK;
 }
 

@@ -211,8 +211,11 @@ def router_weight_grad(ckpt: dict, dlogits: torch.Tensor, parts: int = 1) -> tor
     if parts < 1 or C % parts:
         raise ValueError(f"parts={parts} must divide the {C} columns of dlogits")
     dw = torch.empty((d, C) if parts == 1 else (parts, d, C // parts), dtype=torch.float32, device=dev)
-    check(_lib.load().beam_router_weight_grad(q, scale, T, d, dlogits.data_ptr(), dt, ld, C,
-                                              parts, dw.data_ptr(), _stream(dev)))
+    lib = _lib.load()
+    size = lib.beam_router_weight_grad_workspace(T, d, C)
+    ws = torch.empty((size,), dtype=torch.uint8, device=dev) if size > 0 else None
+    check(lib.beam_router_weight_grad(q, scale, T, d, dlogits.data_ptr(), dt, ld, C, parts, dw.data_ptr(),
+                                      None if ws is None else ws.data_ptr(), size, _stream(dev)))
     return dw
 
 

@@ -579,14 +579,19 @@ beam_status_t beam_checkpoint_route_grad(const int8_t *q_dev, const uint8_t *sca
  * dlogits_dev [T][C], float32 or bfloat16, rows ld_dlogits elements apart:
  * beam_router_weight_grad: dW [d][C] float32 = x^T dlogits with x [T][d] from a checkpoint.  With
  *   parts > 1 (a divisor of C) the columns come as [parts][d][C / parts]: parts = 2 splits
- *   [W_r | W_m], parts = L the L layers of a mask generator.  T = 0 writes zeros.
+ *   [W_r | W_m], parts = L the L layers of a mask generator.  T = 0 writes zeros.  workspace_dev:
+ *   scratch of beam_router_weight_grad_workspace(T, d, C) bytes (0 for many shapes), 16-byte
+ *   aligned, free again when the call's kernels are done.
  * beam_router_input_grad: dx_dev [T][d] float32 = dlogits W^T, w_dev [d][C] float32 or bfloat16,
  *   rows ld_w elements apart.
- * A dlogits or W value that is not finite makes the outputs it reaches NaN.
+ * A dlogits or W value that is not finite makes the outputs it reaches NaN.  Both run on the
+ * tensor cores with float32 accuracy; a bounded device wait that runs out sets the outputs to NaN.
  */
+int64_t beam_router_weight_grad_workspace(int32_t T, int32_t d, int32_t C); /* -1: out of range */
 beam_status_t beam_router_weight_grad(const int8_t *q_dev, const uint8_t *scale_dev, int32_t T,
                                       int32_t d, const void *dlogits_dev, int32_t dtype,
                                       int64_t ld_dlogits, int32_t C, int32_t parts, float *dw_dev,
+                                      void *workspace_dev, int64_t workspace_bytes,
                                       void *stream);
 beam_status_t beam_router_input_grad(const void *dlogits_dev, int32_t dtype, int64_t ld_dlogits,
                                      int32_t T, int32_t C, const void *w_dev, int32_t w_dtype,
