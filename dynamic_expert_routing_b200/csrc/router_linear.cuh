@@ -16,7 +16,7 @@
 // One kernel computes out[m][n] = sum_k A(m, k) B(n, k) on 128 x 128 tiles, 64 of k per step:
 //   dW: m = d, n = c, k = t: A and B lie in memory with m, n contiguous ("MN-major");
 //   dx: m = t, n = d, k = c: k contiguous ("K-major"; MN-major for a repacked W [C][D]).
-// Either way a tile is a block of rows of up to 128 bytes of bf16, and 8 warps write it into
+// Either way a tile is a block of rows of up to 128 bytes of bf16, and 16 warps write it into
 // shared memory in the 128-byte-swizzled layout that tcgen05.mma reads, converting on the way
 // (the operands are not bf16 in memory, so TMA could not bring them); the major-ness is a bit of the
 // instruction descriptor.  Each thread loads the next step's piece as it converts this one's.
@@ -34,8 +34,16 @@ namespace lin {
 constexpr int BM = 128, BN = 128, BK = 64;
 constexpr int kLimbBytes = 128 * BK * 2;      // one limb of one operand's tile
 constexpr int kChain = 4;                     // steps added in the tensor cores' accumulator
-constexpr int kLoadWarps = 8, kEpiWarps = 8;
-constexpr int kThreads = 32 * (kLoadWarps + 1 + kEpiWarps);
+// Warpgroups of 4 warps: 4 that load and convert, one whose first warp issues the MMAs, 2 that drain.
+// The kernel is launched with 72 registers a thread (7 x 128 x 72 of the SM's 65536); the
+// epilogue, which keeps 64 sums per thread, takes some from the others: 512 x 64 + 128 x 40 + 256 x 104
+// = 64512 registers, the launch's own total.
+constexpr int kLoadWarps = 16, kEpiWarps = 8, kMmaWarp = kLoadWarps, kEpiWarp0 = kLoadWarps + 4;
+constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+constexpr int kLaunchRegs = 72, kLoadRegs = 64, kMmaRegs = 40, kEpiRegs = 104;
+static_assert(32 * kLoadWarps * kLoadRegs + 128 * kMmaRegs + 32 * kEpiWarps * kEpiRegs <= kThreads * kLaunchRegs,
+              "the register shares must fit the launch's");
+constexpr int kPieces = 128 * BK / 8 / (32 * kLoadWarps);   // 8-value pieces of a tile per loader thread
 constexpr int kMaxStages = 4;
 constexpr int kSmemLimit = 227 * 1024;
 
@@ -58,7 +66,7 @@ struct Operand {
     const void* p;
     const uint8_t* scale;   // checkpoint: [rows][ld / 32]
     long long ld;           // elements between rows
-    int vec;                // rows 16-byte aligned
+    int vec;                // rows start and end at 16-byte boundaries
 };
 
 struct Params {
@@ -80,43 +88,78 @@ template <> struct Raw<SRC_F32> { uint4 a, b; };
 template <> struct Raw<SRC_BF16> { uint4 a; };
 template <> struct Raw<SRC_CKPT> { uint2 w; int byte; };
 
-__device__ __forceinline__ void raw_zero(Raw<SRC_F32>& r) { r.a = r.b = make_uint4(0u, 0u, 0u, 0u); }
-__device__ __forceinline__ void raw_zero(Raw<SRC_BF16>& r) { r.a = make_uint4(0u, 0u, 0u, 0u); }
-__device__ __forceinline__ void raw_zero(Raw<SRC_CKPT>& r) { r.w = make_uint2(0u, 0u); r.byte = kCkptBias; }
-
-// Columns c .. c + 7 (c a multiple of 8) of a row; zeros from column `cols` on.
-__device__ __forceinline__ void raw_load(Raw<SRC_F32>& r, const Operand& o, long long row, int c, int cols)
+// Loads that a predicate turns into zeros, without a branch: a branch would merge loaded registers
+// with zeroed ones, and the copies would wait for the load that the next step is to use.
+__device__ __forceinline__ uint4 ldg16_if(const void* p, bool on)
 {
-    const float* p = static_cast<const float*>(o.p) + row * o.ld + c;
-    if (o.vec && c + 8 <= cols) {
-        r.a = __ldg(reinterpret_cast<const uint4*>(p));
-        r.b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    uint4 r;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+                 "mov.b32 %0, 0; mov.b32 %1, 0; mov.b32 %2, 0; mov.b32 %3, 0;\n\t"
+                 "@p ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+                 : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w) : "l"(p), "r"((int)on));
+    return r;
+}
+__device__ __forceinline__ uint2 ldg8_if(const void* p, bool on)
+{
+    uint2 r;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.b32 %0, 0; mov.b32 %1, 0;\n\t"
+                 "@p ld.global.nc.v2.u32 {%0,%1}, [%2];\n\t}"
+                 : "=&r"(r.x), "=&r"(r.y) : "l"(p), "r"((int)on));
+    return r;
+}
+__device__ __forceinline__ uint32_t ldg4_if(const void* p, bool on)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t"
+                 "@p ld.global.nc.u32 %0, [%1];\n\t}" : "=&r"(r) : "l"(p), "r"((int)on));
+    return r;
+}
+__device__ __forceinline__ uint32_t ldg2_if(const void* p, bool on)
+{
+    unsigned short r;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b16 %0, 0;\n\t"
+                 "@p ld.global.nc.u16 %0, [%1];\n\t}" : "=&h"(r) : "l"(p), "r"((int)on));
+    return r;
+}
+__device__ __forceinline__ int ldg1_if(const void* p, bool on)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t"
+                 "@p ld.global.nc.u8 %0, [%1];\n\t}" : "=&r"(r) : "l"(p), "r"((int)on));
+    return (int)r;
+}
+
+// The first n values from p on (n <= 0: none), the rest 0.  VEC: p is 16-byte aligned and n ends at a
+// 16-byte boundary.
+template <bool VEC>
+__device__ __forceinline__ void raw_load(Raw<SRC_F32>& r, const char* p, const uint8_t*, int n)
+{
+    if (VEC) {
+        r.a = ldg16_if(p, n > 0);
+        r.b = ldg16_if(p + 16, n > 4);
     } else {
-        const uint32_t* u = reinterpret_cast<const uint32_t*>(p);
-        uint32_t v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? __ldg(u + j) : 0u;
-        r.a = make_uint4(v[0], v[1], v[2], v[3]);
-        r.b = make_uint4(v[4], v[5], v[6], v[7]);
+        r.a = make_uint4(ldg4_if(p, n > 0), ldg4_if(p + 4, n > 1), ldg4_if(p + 8, n > 2), ldg4_if(p + 12, n > 3));
+        r.b = make_uint4(ldg4_if(p + 16, n > 4), ldg4_if(p + 20, n > 5), ldg4_if(p + 24, n > 6), ldg4_if(p + 28, n > 7));
     }
 }
-__device__ __forceinline__ void raw_load(Raw<SRC_BF16>& r, const Operand& o, long long row, int c, int cols)
+template <bool VEC>
+__device__ __forceinline__ void raw_load(Raw<SRC_BF16>& r, const char* p, const uint8_t*, int n)
 {
-    const unsigned short* p = static_cast<const unsigned short*>(o.p) + row * o.ld + c;
-    if (o.vec && c + 8 <= cols) {
-        r.a = __ldg(reinterpret_cast<const uint4*>(p));
+    if (VEC) {
+        r.a = ldg16_if(p, n > 0);
     } else {
         uint32_t v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? __ldg(p + j) : 0u;
+        for (int j = 0; j < 8; ++j) v[j] = ldg2_if(p + 2 * j, n > j);
         r.a = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
     }
 }
-// Checkpoint rows are padded with zeros to whole blocks, so no column past `cols` needs a test.
-__device__ __forceinline__ void raw_load(Raw<SRC_CKPT>& r, const Operand& o, long long row, int c, int)
+// Checkpoint rows are 32-byte aligned and padded with zeros to whole blocks.
+template <bool VEC>
+__device__ __forceinline__ void raw_load(Raw<SRC_CKPT>& r, const char* p, const uint8_t* scale, int n)
 {
-    r.w = __ldg(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(o.p) + row * o.ld + c));
-    r.byte = __ldg(o.scale + row * (o.ld / kCkptBlock) + c / kCkptBlock);
+    r.w = ldg8_if(p, n > 0);
+    r.byte = ldg1_if(scale, n > 0);
 }
 
 // The upper halves of two words.
@@ -166,46 +209,57 @@ __device__ __forceinline__ bool get_unit(const Params& p, int u, Unit& t)
     return true;
 }
 
-// The piece i (0..3) of a tile that loader thread `tid` handles: row and 8-column chunk of the
-// tile's block of rows.  MN-major: 64 rows (k) x 16 chunks (two 64-wide blocks); K-major: 128 rows x
-// 8 chunks.  A quarter warp stores 8 different chunks of one row: no bank conflict.
-template <bool MN> struct Piece {
-    int row, chunk;
-    __device__ Piece(int tid, int i)
+// The pieces of one operand's tiles that a loader thread brings: one 8-value chunk of kPieces rows of
+// the tile's block of rows.  MN-major: 64 rows (k) x 16 chunks (two 64-wide blocks); K-major: 128 rows
+// (m or n) x 8 chunks.  A quarter warp stores 8 different chunks of one row: no bank conflict.
+// Rows and columns past the operand read as zero (only k needs it: the others' outputs are never
+// stored).
+template <int SRC, bool MN> struct Cursor {
+    static constexpr int ES = SRC == SRC_CKPT ? 1 : (SRC == SRC_F32 ? 4 : 2);
+    static constexpr int kRows = 32 * kLoadWarps / (MN ? 16 : 8);   // rows of the block between pieces
+    const char* p;           // piece 0 of the current step
+    const uint8_t* sc;
+    int x, k;                // first m or n of piece 0, and its first k
+    __device__ __forceinline__ void start(const Operand& o, int tid, int x0, int k0)
     {
-        if (MN) { chunk = tid & 15; row = (tid >> 4) + 16 * i; }
-        else { chunk = tid & 7; row = (tid >> 3) + 32 * i; }
+        const int chunk = MN ? (tid & 15) : (tid & 7), row = MN ? (tid >> 4) : (tid >> 3);
+        x = x0 + (MN ? 8 * chunk : row);
+        k = k0 + (MN ? row : 8 * chunk);
+        const long long r = MN ? k : x, c = MN ? x : k;
+        p = static_cast<const char*>(o.p) + (r * o.ld + c) * ES;
+        if (SRC == SRC_CKPT) sc = o.scale + r * (o.ld >> 5) + (c >> 5);
     }
-    __device__ uint32_t offset() const
+    __device__ __forceinline__ void advance(const Operand& o)
     {
-        return (MN ? (chunk >> 3) * (BK * 128) : 0) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+        k += BK;
+        p += (MN ? BK * o.ld : BK) * ES;
+        if (SRC == SRC_CKPT) sc += MN ? BK * (o.ld >> 5) : BK >> 5;
+    }
+    // xs and K: the limits of m or n, and of k (0: nothing is read)
+    template <bool VEC> __device__ __forceinline__ void load(Raw<SRC>& r, const Operand& o, int i, int xs, int K) const
+    {
+        const int xi = MN ? x : x + i * kRows, ki = MN ? k + i * kRows : k;
+        raw_load<VEC>(r, p + i * kRows * o.ld * ES, sc + i * kRows * (o.ld >> 5),
+                      xi < xs && ki < K ? (MN ? xs - x : K - k) : 0);
     }
 };
+static_assert(kCkptBlock == 32, "the scale of a value is found by shifts of 5");
 
-// One operand of one step: x0 = first m or n of the tile, xs its limit (past it nothing is read:
-// those outputs are never stored), xw the tile's width, k0 the first k.
-template <int SRC, bool MN>
-__device__ __forceinline__ void piece_load(Raw<SRC>& r, const Operand& o, const Piece<MN>& p, int x0, int xs,
-                                           int k0, int K)
+// Byte offset of a thread's piece 0 in the swizzled tile; piece i is kRows * 128 bytes on (a
+// multiple of the 8-row swizzle period).
+template <bool MN> __device__ __forceinline__ uint32_t piece_offset(int tid)
 {
-    if (MN) {
-        const int k = k0 + p.row, x = x0 + 8 * p.chunk;
-        if (k < K && x < xs) raw_load(r, o, k, x, xs);
-        else raw_zero(r);
-    } else {
-        const int k = k0 + 8 * p.chunk, x = x0 + p.row;
-        if (k < K && x < xs) raw_load(r, o, x, k, K);
-        else raw_zero(r);
-    }
+    const int chunk = MN ? (tid & 15) : (tid & 7), row = MN ? (tid >> 4) : (tid >> 3);
+    return (MN ? (chunk >> 3) * (BK * 128) : 0) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
 }
 
-template <int SRC, bool MN>
-__device__ __forceinline__ void piece_store(const Raw<SRC>& r, uint8_t* tile, const Piece<MN>& p)
+template <int SRC>
+__device__ __forceinline__ void piece_store(const Raw<SRC>& r, uint8_t* at)
 {
     uint4 l[limbs(SRC)];
     raw_limbs(r, l);
 #pragma unroll
-    for (int i = 0; i < limbs(SRC); ++i) *reinterpret_cast<uint4*>(tile + i * kLimbBytes + p.offset()) = l[i];
+    for (int i = 0; i < limbs(SRC); ++i) *reinterpret_cast<uint4*>(at + i * kLimbBytes) = l[i];
 }
 
 // Shared-memory descriptor of an MN-major tile: blocks of 64 values (128 bytes) of m or n, 64 rows of k
@@ -228,7 +282,7 @@ __device__ __forceinline__ void store8(float* p, const float* v, int n)
     }
 }
 
-template <int SA, bool MNA, int SB, bool MNB>
+template <int SA, bool MNA, int SB, bool MNB, bool VEC>
 __global__ void __launch_bounds__(kThreads, 1)
 lin_gemm_kernel(const __grid_constant__ Params p)
 {
@@ -256,7 +310,7 @@ lin_gemm_kernel(const __grid_constant__ Params p)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    if (warp == kLoadWarps) {
+    if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      ::"r"(tc::smem_u32(tmem_slot)), "r"(kTmemCols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -269,52 +323,59 @@ lin_gemm_kernel(const __grid_constant__ Params p)
 
     if (warp < kLoadWarps) {
         // ------------------------------------------------ loaders: global -> bf16 limbs -> shared
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
         const int tid = threadIdx.x;
-        Raw<SA> ra[4];
-        Raw<SB> rb[4];
+        const uint32_t oa = piece_offset<MNA>(tid), ob = piece_offset<MNB>(tid) + LA * kLimbBytes;
+        Cursor<SA, MNA> ca;
+        Cursor<SB, MNB> cb;
+        Raw<SA> ra[kPieces];
+        Raw<SB> rb[kPieces];
         Unit t;
-        int u = blockIdx.x, step = 0;
-        bool has = get_unit(p, u, t);
-        if (has) {
-            step = t.s0;
+        int u = blockIdx.x, left = 0;
+        auto start = [&]() {
+            if (!get_unit(p, u, t)) return false;
+            ca.start(p.a, tid, t.m0, t.s0 * BK);
+            cb.start(p.b, tid, t.n0, t.s0 * BK);
+            left = t.s1 - t.s0;
+            return true;
+        };
+        bool has = start();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                piece_load<SA, MNA>(ra[i], p.a, Piece<MNA>(tid, i), t.m0, p.M, step * BK, p.K);
-                piece_load<SB, MNB>(rb[i], p.b, Piece<MNB>(tid, i), t.n0, p.N, step * BK, p.K);
-            }
+        for (int i = 0; i < kPieces; ++i) {   // a unit for every block: the grid is at most the units
+            ca.template load<VEC>(ra[i], p.a, i, p.M, p.K);
+            cb.template load<VEC>(rb[i], p.b, i, p.N, p.K);
         }
         int s = 0;
         uint32_t ph = 0;
         while (has) {
-            // the step after this one
-            if (++step >= t.s1) {
+            // the cursors move on to the step after this one
+            if (--left > 0) {
+                ca.advance(p.a);
+                cb.advance(p.b);
+            } else {
                 u += gridDim.x;
-                has = get_unit(p, u, t);
-                if (has) step = t.s0;
+                has = start();
             }
             if (!tc::mbar_wait(empty_bar(s), ph ^ 1u, abort_flag)) break;
-            uint8_t* sa = gbase + s * stage_bytes<SA, SB>();
-            uint8_t* sb = sa + LA * kLimbBytes;
+            uint8_t* sm = gbase + s * stage_bytes<SA, SB>();
+            const int k_end = has ? p.K : 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const Piece<MNA> pa(tid, i);
-                const Piece<MNB> pb(tid, i);
-                const Raw<SA> ca = ra[i];
-                const Raw<SB> cb = rb[i];
-                if (has) {
-                    piece_load<SA, MNA>(ra[i], p.a, pa, t.m0, p.M, step * BK, p.K);
-                    piece_load<SB, MNB>(rb[i], p.b, pb, t.n0, p.N, step * BK, p.K);
-                }
-                piece_store<SA, MNA>(ca, sa, pa);
-                piece_store<SB, MNB>(cb, sb, pb);
+            for (int i = 0; i < kPieces; ++i) {
+                const Raw<SA> va = ra[i];
+                const Raw<SB> vb = rb[i];
+                ca.template load<VEC>(ra[i], p.a, i, p.M, k_end);
+                cb.template load<VEC>(rb[i], p.b, i, p.N, k_end);
+                piece_store<SA>(va, sm + oa + i * (Cursor<SA, MNA>::kRows * 128));
+                piece_store<SB>(vb, sm + ob + i * (Cursor<SB, MNB>::kRows * 128));
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(full_bar(s));
             if (++s == ST) { s = 0; ph ^= 1u; }
         }
-    } else if (warp == kLoadWarps) {
-        if (lane == 0) {
+    } else if (warp < kEpiWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+        if (warp == kMmaWarp && lane == 0) {
             // -------------------------------------------- MMA issuer
             int s = 0, buf = 0;
             uint32_t ph = 0, bph = 0;
@@ -371,8 +432,9 @@ lin_gemm_kernel(const __grid_constant__ Params p)
         }
     } else {
         // ------------------------------------------------ epilogue: TMEM -> float32 sums -> global
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
         const int lb = 32 * (warp & 3);                    // TMEM lanes this warp may access
-        const int half = (warp - kLoadWarps - 1) / 4;      // which 64 columns
+        const int half = (warp - kEpiWarp0) / 4;           // which 64 columns
         int buf = 0;
         uint32_t bph = 0;
         bool ok = true;
@@ -429,7 +491,7 @@ lin_gemm_kernel(const __grid_constant__ Params p)
     }
     tc::tc_fence_before();
     __syncthreads();
-    if (warp == kLoadWarps) {
+    if (warp == kMmaWarp) {
         __syncwarp();
         tc::tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");

@@ -337,15 +337,16 @@ static lin::Params lin_params(int M, int N, int K)
     return p;
 }
 
-static lin::Operand operand(const void* x, int dtype, long long ld)
+static lin::Operand operand(const void* x, int dtype, long long ld, long long cols)
 {
-    return {x, nullptr, ld, !misaligned(x, 16) && ld % (16 / elem_size(dtype)) == 0};
+    const int v = 16 / elem_size(dtype);
+    return {x, nullptr, ld, !misaligned(x, 16) && ld % v == 0 && cols % v == 0};
 }
 
-template <int SA, bool MNA, int SB, bool MNB>
-static cudaError_t launch_lin(const lin::Params& p, int sms, cudaStream_t st)
+template <int SA, bool MNA, int SB, bool MNB, bool VEC>
+static cudaError_t launch_lin_vec(const lin::Params& p, int sms, cudaStream_t st)
 {
-    auto kernel = lin::lin_gemm_kernel<SA, MNA, SB, MNB>;
+    auto kernel = lin::lin_gemm_kernel<SA, MNA, SB, MNB, VEC>;
     constexpr int smem = lin::smem_bytes<SA, SB>();
     static std::atomic<unsigned long long> ready;   // devices whose attribute is set
     int dev = 0;
@@ -357,6 +358,13 @@ static cudaError_t launch_lin(const lin::Params& p, int sms, cudaStream_t st)
         if (dev < 64) ready.fetch_or(1ULL << dev, std::memory_order_relaxed);
     }
     return launch_free(kernel, dim3((unsigned)std::min(p.units, sms)), dim3(lin::kThreads), smem, st, p);
+}
+
+template <int SA, bool MNA, int SB, bool MNB>
+static cudaError_t launch_lin(const lin::Params& p, int sms, cudaStream_t st)
+{
+    return p.a.vec && p.b.vec ? launch_lin_vec<SA, MNA, SB, MNB, true>(p, sms, st)
+                              : launch_lin_vec<SA, MNA, SB, MNB, false>(p, sms, st);
 }
 
 // Workspace of the weight gradient: the slices' partial tiles.
@@ -411,7 +419,7 @@ beam_status_t beam_router_weight_grad(const int8_t* q, const uint8_t* scale, int
     if (need > 0 && (!workspace || workspace_bytes < need || misaligned(workspace, 16)))
         FAIL_ARG("the workspace must be 16-byte aligned and hold %lld bytes", need);
     p.a = {q, scale, ceil_div(d, kCkptBlock) * kCkptBlock, 1};
-    p.b = operand(dlogits, dtype, ld_dlogits);
+    p.b = operand(dlogits, dtype, ld_dlogits, C);
     const int ldp = weight_ld(C), cp = C / parts;
     p.out = need ? static_cast<float*>(workspace) : dw;
     p.slice = (long long)d * ldp;
@@ -439,8 +447,8 @@ beam_status_t beam_router_input_grad(const void* dlogits, int32_t dtype, int64_t
     if (T == 0) return BEAM_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     lin::Params p = lin_params(T, d, C);
-    p.a = operand(dlogits, dtype, ld_dlogits);
-    p.b = operand(w, w_dtype, ld_w);
+    p.a = operand(dlogits, dtype, ld_dlogits, C);
+    p.b = operand(w, w_dtype, ld_w, C);
     p.out = dx;
     p.cp = d;
     const int sms = num_sms();
