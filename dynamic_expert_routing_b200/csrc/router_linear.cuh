@@ -375,8 +375,13 @@ lin_gemm_kernel(const __grid_constant__ Params p)
         }
     } else if (warp < kEpiWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
-        if (warp == kMmaWarp && lane == 0) {
-            // -------------------------------------------- MMA issuer
+        if (warp == kMmaWarp) {
+            // -------------------------------------------- MMA issuer.  The whole warp walks the
+            // steps, so that descriptors stay in uniform registers; one elected lane issues.
+            // The descriptors of a stage differ from the first stage's in the address field alone.
+            const bool leader = tc::elect_one();
+            const uint64_t da = MNA ? mn_desc(base) : tc::sw128_desc(base);
+            const uint64_t db = MNB ? mn_desc(base + LA * kLimbBytes) : tc::sw128_desc(base + LA * kLimbBytes);
             int s = 0, buf = 0;
             uint32_t ph = 0, bph = 0;
             bool ok = true, issued = false;
@@ -384,51 +389,59 @@ lin_gemm_kernel(const __grid_constant__ Params p)
             for (int u = blockIdx.x; ok && get_unit(p, u, t); u += gridDim.x) {
                 const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((MNA ? 1u : 0u) << 15) |
                                        ((MNB ? 1u : 0u) << 16) | ((uint32_t)(t.nt >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+                int at = 0;
                 for (int step = t.s0; step < t.s1; ++step) {
-                    const int at = (step - t.s0) % kChain;
                     const uint32_t d0 = tmem_base + (uint32_t)(buf * ACC * BN);
                     if (at == 0) {
                         if (!tc::mbar_wait(tempty_bar(buf), bph ^ 1u, abort_flag)) { ok = false; break; }
                     }
                     if (!tc::mbar_wait(full_bar(s), ph, abort_flag)) { ok = false; break; }
                     tc::tc_fence_after();
-                    const uint32_t sa = base + s * stage_bytes<SA, SB>(), sb = sa + LA * kLimbBytes;
-                    const int n16 = (min(BK, p.K - step * BK) + 15) / 16;
-                    for (int kk = 0; kk < n16; ++kk) {
-                        const bool first = at == 0 && kk == 0;
-                        bool first_low = first;
+                    const uint64_t sa = da + (uint32_t)(s * (stage_bytes<SA, SB>() >> 4));
+                    const uint64_t sb = db + (uint32_t)(s * (stage_bytes<SA, SB>() >> 4));
+                    const int k_left = p.K - step * BK;
+                    if (leader) {
 #pragma unroll
-                        for (int i = 0; i < LA; ++i)
+                        for (int kk = 0; kk < BK / 16; ++kk) {
+                            if (16 * kk >= k_left) break;
+                            // 16 of k: 32 bytes of a K-major row, 16 rows of an MN-major block
+                            constexpr int KA = (MNA ? 2048 : 32) >> 4, KB = (MNB ? 2048 : 32) >> 4;
+                            bool low = false;   // whether a small product of this kk was issued
 #pragma unroll
-                            for (int j = 0; j < LB; ++j) {
-                                if (i + j >= (LA > LB ? LA : LB)) continue;
-                                // 16 of k: 32 bytes of a K-major row, 16 rows of an MN-major block
-                                const uint64_t ad = MNA ? mn_desc(sa + i * kLimbBytes + kk * 2048)
-                                                        : tc::sw128_desc(sa + i * kLimbBytes) + 2ull * kk;
-                                const uint64_t bd = MNB ? mn_desc(sb + j * kLimbBytes + kk * 2048)
-                                                        : tc::sw128_desc(sb + j * kLimbBytes) + 2ull * kk;
-                                if (i + j == 0) {
-                                    tc::tc_mma_f16(d0, ad, bd, idesc, first ? 0u : 1u);
-                                } else {
-                                    tc::tc_mma_f16(d0 + BN, ad, bd, idesc, first_low ? 0u : 1u);
-                                    first_low = false;
+                            for (int i = 0; i < LA; ++i)
+#pragma unroll
+                                for (int j = 0; j < LB; ++j) {
+                                    if (i + j >= (LA > LB ? LA : LB)) continue;
+                                    const uint64_t ad = sa + (uint32_t)(i * (kLimbBytes >> 4) + kk * KA);
+                                    const uint64_t bd = sb + (uint32_t)(j * (kLimbBytes >> 4) + kk * KB);
+                                    const bool add = kk > 0 || at > 0;
+                                    if (i + j == 0) {
+                                        tc::tc_mma_f16(d0, ad, bd, idesc, add);
+                                    } else {
+                                        tc::tc_mma_f16(d0 + BN, ad, bd, idesc, add || low);
+                                        low = true;
+                                    }
                                 }
-                            }
+                        }
+                        tc::tc_commit(empty_bar(s));
                     }
                     issued = true;
-                    tc::tc_commit(empty_bar(s));
+                    __syncwarp();
                     if (++s == ST) { s = 0; ph ^= 1u; }
-                    if (at == kChain - 1 || step + 1 == t.s1) {
-                        tc::tc_commit(tfull_bar(buf));
+                    if (++at == kChain || step + 1 == t.s1) {
+                        if (leader) tc::tc_commit(tfull_bar(buf));
+                        __syncwarp();
+                        at = 0;
                         if (++buf == 2) { buf = 0; bph ^= 1u; }
                     }
                 }
             }
-            if (!ok && issued) {
+            if (!ok && issued && leader) {
                 tc::tc_commit(drain_bar);   // completes when every MMA issued so far has finished
                 const unsigned long long t0 = tc::globaltimer();
                 while (!tc::mbar_try_wait(drain_bar, 0) && tc::globaltimer() - t0 < tc::kWaitLimitNs) {}
             }
+            __syncwarp();
         }
     } else {
         // ------------------------------------------------ epilogue: TMEM -> float32 sums -> global
