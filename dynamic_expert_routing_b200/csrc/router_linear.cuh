@@ -13,26 +13,30 @@
 // its own (the small ones share another), and every kChain steps of 64 the accumulators are
 // drained into float32 sums in registers, rounded to nearest.
 //
-// One kernel computes out[m][n] = sum_k A(m, k) B(n, k) on 128 x 128 tiles, 64 of k per step:
+// One kernel computes out[m][n] = sum_k A(m, k) B(n, k) on 256 x 128 tiles, 64 of k per step:
 //   dW: m = d, n = c, k = t: A and B lie in memory with m, n contiguous ("MN-major");
 //   dx: m = t, n = d, k = c: k contiguous ("K-major"; MN-major for a repacked W [C][D]).
-// Either way a tile is a block of rows of up to 128 bytes of bf16, and 16 warps write it into
-// shared memory in the 128-byte-swizzled layout that tcgen05.mma reads, converting on the way
-// (the operands are not bf16 in memory, so TMA could not bring them); the major-ness is a bit of the
-// instruction descriptor.  Each thread loads the next step's piece as it converts this one's.
-// One warp issues the MMAs; 8 warps drain TMEM (two accumulator sets, so that a drain overlaps the
-// next steps) and store.  The grid is persistent; when the tiles are fewer than the SMs, k is cut
-// into slices whose partial tiles lin_reduce_kernel adds in order.
+// Two CTAs share a tile (cta_group::2): each converts its 128 rows of A and half of B, so an operand
+// value is converted half as often, which is what bounds the kernel beside the MMAs: the operands are
+// not bf16 in memory, so TMA could not bring them.  16 warps per CTA write them into shared memory in
+// the 128-byte-swizzled layout that tcgen05.mma reads (a block of rows of 128 bytes; the major-ness
+// is a bit of the instruction descriptor); each thread loads the next step's piece as it converts
+// this one's.  One warp of the first CTA issues the MMAs of both; 8 warps in each drain its rows'
+// accumulators from TMEM (two sets, so that a drain overlaps the next steps) and store.  The grid is
+// persistent; when the tiles are fewer than the CTA pairs, k is cut into slices whose partial tiles
+// lin_reduce_kernel adds in order.
 // Every wait is bounded: when one runs out, the kernel's outputs are set to NaN.
 #pragma once
+#include <type_traits>
 #include "checkpoint.cuh"
 #include "tc_ptx.cuh"
 
 namespace beam {
 namespace lin {
 
-constexpr int BM = 128, BN = 128, BK = 64;
-constexpr int kLimbBytes = 128 * BK * 2;      // one limb of one operand's tile
+constexpr int BM = 256, BN = 128, BK = 64;    // the tile of a CTA pair
+constexpr int kRowsA = BM / 2, kRowsB = BN / 2;   // a CTA's share of the operands
+constexpr int kLimbA = kRowsA * BK * 2, kLimbB = kRowsB * BK * 2;   // bytes of one limb of a share
 constexpr int kChain = 4;                     // steps added in the tensor cores' accumulator
 // Warpgroups of 4 warps: 4 that load and convert, one whose first warp issues the MMAs, 2 that drain.
 // The kernel is launched with 72 registers a thread (7 x 128 x 72 of the SM's 65536); the
@@ -43,23 +47,24 @@ constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kLaunchRegs = 72, kLoadRegs = 64, kMmaRegs = 40, kEpiRegs = 104;
 static_assert(32 * kLoadWarps * kLoadRegs + 128 * kMmaRegs + 32 * kEpiWarps * kEpiRegs <= kThreads * kLaunchRegs,
               "the register shares must fit the launch's");
-constexpr int kPieces = 128 * BK / 8 / (32 * kLoadWarps);   // 8-value pieces of a tile per loader thread
 constexpr int kMaxStages = 4;
+constexpr int kStagePitch = 33;               // epilogue staging: 32 x 32 sub-tiles, conflict-free both ways
+constexpr int kEpiBytes = kEpiWarps * 32 * kStagePitch * 4;
 constexpr int kSmemLimit = 227 * 1024;
 
 enum Src { SRC_CKPT = 0, SRC_F32 = 1, SRC_BF16 = 2 };
 __host__ __device__ constexpr int limbs(int src) { return src == SRC_F32 ? 3 : 1; }
 
-template <int SA, int SB> __host__ __device__ constexpr int stage_bytes() { return (limbs(SA) + limbs(SB)) * kLimbBytes; }
+template <int SA, int SB> __host__ __device__ constexpr int stage_bytes() { return limbs(SA) * kLimbA + limbs(SB) * kLimbB; }
 template <int SA, int SB> __host__ __device__ constexpr int stages()
 {
-    constexpr int n = (kSmemLimit - 2048) / stage_bytes<SA, SB>();
+    constexpr int n = (kSmemLimit - kEpiBytes - 2048) / stage_bytes<SA, SB>();
     return n < kMaxStages ? n : kMaxStages;
 }
 template <int SA, int SB> __host__ __device__ constexpr int accs() { return limbs(SA) * limbs(SB) > 1 ? 2 : 1; }
 template <int SA, int SB> __host__ __device__ constexpr int smem_bytes()
 {
-    return stages<SA, SB>() * stage_bytes<SA, SB>() + 1024 /* alignment */ + 256 /* barriers */;
+    return stages<SA, SB>() * stage_bytes<SA, SB>() + kEpiBytes + 1024 /* alignment */ + 256 /* barriers */;
 }
 
 struct Operand {
@@ -129,6 +134,22 @@ __device__ __forceinline__ int ldg1_if(const void* p, bool on)
     return (int)r;
 }
 
+// Eight values, all of them there (off: the distance of the second half where it exists, else 0).
+__device__ __forceinline__ void raw_load_all(Raw<SRC_F32>& r, const char* p, const uint8_t*, int off)
+{
+    r.a = __ldg(reinterpret_cast<const uint4*>(p));
+    r.b = __ldg(reinterpret_cast<const uint4*>(p + off));
+}
+__device__ __forceinline__ void raw_load_all(Raw<SRC_BF16>& r, const char* p, const uint8_t*, int)
+{
+    r.a = __ldg(reinterpret_cast<const uint4*>(p));
+}
+__device__ __forceinline__ void raw_load_all(Raw<SRC_CKPT>& r, const char* p, const uint8_t* scale, int)
+{
+    r.w = __ldg(reinterpret_cast<const uint2*>(p));
+    r.byte = __ldg(scale);
+}
+
 // The first n values from p on (n <= 0: none), the rest 0.  VEC: p is 16-byte aligned and n ends at a
 // 16-byte boundary.
 template <bool VEC>
@@ -194,7 +215,7 @@ __device__ __forceinline__ void raw_limbs(const Raw<SRC_F32>& r, uint4* o)
 }
 
 // ---------------------------------------------------------------- units and steps
-struct Unit { int m0, n0, nt, slice, s0, s1; };
+struct Unit { int m0, n0, slice, s0, s1; };
 
 __device__ __forceinline__ bool get_unit(const Params& p, int u, Unit& t)
 {
@@ -205,29 +226,35 @@ __device__ __forceinline__ bool get_unit(const Params& p, int u, Unit& t)
     t.slice = r / p.m_tiles;
     t.s0 = t.slice * p.split_steps;
     t.s1 = min(p.k_steps, t.s0 + p.split_steps);
-    t.nt = min(BN, (p.N - t.n0 + 63) & ~63);
     return true;
 }
 
-// The pieces of one operand's tiles that a loader thread brings: one 8-value chunk of kPieces rows of
-// the tile's block of rows.  MN-major: 64 rows (k) x 16 chunks (two 64-wide blocks); K-major: 128 rows
-// (m or n) x 8 chunks.  A quarter warp stores 8 different chunks of one row: no bank conflict.
-// Rows and columns past the operand read as zero (only k needs it: the others' outputs are never
-// stored).
-template <int SRC, bool MN> struct Cursor {
+// The pieces of one operand share (ROWS of m or n) that a loader thread brings: one 8-value chunk of
+// kPieces rows of the share's blocks of rows.  MN-major: 64 rows (k) x ROWS / 8 chunks; K-major: ROWS
+// rows (m or n) x 8 chunks.  A quarter warp stores 8 different chunks of one row: no bank conflict.
+// Past the operand, k reads as zero; m and n read anything (those outputs are never stored).
+template <int SRC, bool MN, int ROWS> struct Cursor {
     static constexpr int ES = SRC == SRC_CKPT ? 1 : (SRC == SRC_F32 ? 4 : 2);
-    static constexpr int kRows = 32 * kLoadWarps / (MN ? 16 : 8);   // rows of the block between pieces
+    static constexpr int kChunks = MN ? ROWS / 8 : 8;
+    static constexpr int kRows = 32 * kLoadWarps / kChunks;        // rows of a block between pieces
+    static constexpr int kPieces = (MN ? BK : ROWS) / kRows;
     const char* p;           // piece 0 of the current step
     const uint8_t* sc;
-    int x, k;                // first m or n of piece 0, and its first k
-    __device__ __forceinline__ void start(const Operand& o, int tid, int x0, int k0)
+    int k;                   // its first k
+    int n;                   // MN-major: values that the chunk has (<= 0: none);  K-major: rows from piece 0 on
+    int off;                 // distance of a chunk's second 16 bytes
+    __device__ __forceinline__ void start(const Operand& o, int tid, int x0, int xs, int k0)
     {
-        const int chunk = MN ? (tid & 15) : (tid & 7), row = MN ? (tid >> 4) : (tid >> 3);
-        x = x0 + (MN ? 8 * chunk : row);
+        const int chunk = tid % kChunks, row = tid / kChunks;
+        int x = x0 + (MN ? 8 * chunk : row);
         k = k0 + (MN ? row : 8 * chunk);
+        n = xs - x;
+        off = !MN || n > 4 ? 16 : 0;
+        if (n <= 0) { x = MN ? (xs - 1) & ~7 : xs - 1; off = 0; }   // a place that can be read
         const long long r = MN ? k : x, c = MN ? x : k;
         p = static_cast<const char*>(o.p) + (r * o.ld + c) * ES;
         if (SRC == SRC_CKPT) sc = o.scale + r * (o.ld >> 5) + (c >> 5);
+        if (!MN && n <= 0) off = 16;
     }
     __device__ __forceinline__ void advance(const Operand& o)
     {
@@ -235,31 +262,35 @@ template <int SRC, bool MN> struct Cursor {
         p += (MN ? BK * o.ld : BK) * ES;
         if (SRC == SRC_CKPT) sc += MN ? BK * (o.ld >> 5) : BK >> 5;
     }
-    // xs and K: the limits of m or n, and of k (0: nothing is read)
-    template <bool VEC> __device__ __forceinline__ void load(Raw<SRC>& r, const Operand& o, int i, int xs, int K) const
+    // Piece i where the whole step lies inside k.
+    __device__ __forceinline__ void load_all(Raw<SRC>& r, const Operand& o, int i) const
     {
-        const int xi = MN ? x : x + i * kRows, ki = MN ? k + i * kRows : k;
+        const long long d = MN || i * kRows < n ? i * kRows : 0;
+        raw_load_all(r, p + d * o.ld * ES, sc + d * (o.ld >> 5), off);
+    }
+    template <bool VEC> __device__ __forceinline__ void load(Raw<SRC>& r, const Operand& o, int i, int K) const
+    {
+        const int ki = MN ? k + i * kRows : k, have = MN ? n : n - i * kRows;
         raw_load<VEC>(r, p + i * kRows * o.ld * ES, sc + i * kRows * (o.ld >> 5),
-                      xi < xs && ki < K ? (MN ? xs - x : K - k) : 0);
+                      have > 0 && ki < K ? (MN ? n : K - k) : 0);
+    }
+    // Byte offset of piece 0 in a limb's swizzled tile; piece i is kRows * 128 bytes on (a multiple of
+    // the 8-row swizzle period).
+    __device__ static __forceinline__ uint32_t offset(int tid)
+    {
+        const int chunk = tid % kChunks, row = tid / kChunks;
+        return (chunk >> 3) * (BK * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
     }
 };
 static_assert(kCkptBlock == 32, "the scale of a value is found by shifts of 5");
 
-// Byte offset of a thread's piece 0 in the swizzled tile; piece i is kRows * 128 bytes on (a
-// multiple of the 8-row swizzle period).
-template <bool MN> __device__ __forceinline__ uint32_t piece_offset(int tid)
-{
-    const int chunk = MN ? (tid & 15) : (tid & 7), row = MN ? (tid >> 4) : (tid >> 3);
-    return (MN ? (chunk >> 3) * (BK * 128) : 0) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
-}
-
-template <int SRC>
+template <int SRC, int LIMB>
 __device__ __forceinline__ void piece_store(const Raw<SRC>& r, uint8_t* at)
 {
     uint4 l[limbs(SRC)];
     raw_limbs(r, l);
 #pragma unroll
-    for (int i = 0; i < limbs(SRC); ++i) *reinterpret_cast<uint4*>(at + i * kLimbBytes) = l[i];
+    for (int i = 0; i < limbs(SRC); ++i) *reinterpret_cast<uint4*>(at + i * LIMB) = l[i];
 }
 
 // Shared-memory descriptor of an MN-major tile: blocks of 64 values (128 bytes) of m or n, 64 rows of k
@@ -269,54 +300,47 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t saddr)
     return tc::sw128_desc(saddr) - ((uint64_t)1 << 16) + ((uint64_t)((BK * 128) >> 4) << 16);
 }
 
-// 32 bytes in one store (a whole sector) where the address allows, else one value at a time.
-__device__ __forceinline__ void store8(float* p, const float* v, int n)
-{
-    if (n >= 8 && (reinterpret_cast<uintptr_t>(p) & 31) == 0) {
-        asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
-                     "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]) : "memory");
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < n) p[j] = v[j];
-    }
-}
-
 template <int SA, bool MNA, int SB, bool MNB, bool VEC>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 lin_gemm_kernel(const __grid_constant__ Params p)
 {
     constexpr int LA = limbs(SA), LB = limbs(SB), ST = stages<SA, SB>(), ACC = accs<SA, SB>();
-    constexpr int kTmemCols = 2 * ACC * BN;
+    constexpr int kTmemCols = 512;   // 2 sets of ACC accumulators of BN columns, at the same place in both CTAs
+    static_assert(2 * ACC * BN <= kTmemCols, "accumulators");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = tc::smem_u32(smem_raw);
     const uint32_t base = (raw_addr + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - raw_addr);
-    const uint32_t bars = base + ST * stage_bytes<SA, SB>();
+    float* epi_buf = reinterpret_cast<float*>(gbase + ST * stage_bytes<SA, SB>());
+    const uint32_t bars = base + ST * stage_bytes<SA, SB>() + kEpiBytes;
     auto full_bar = [&](int s) { return bars + 8u * s; };
     auto empty_bar = [&](int s) { return bars + 8u * (ST + s); };
     auto tfull_bar = [&](int a) { return bars + 8u * (2 * ST + a); };
     auto tempty_bar = [&](int a) { return bars + 8u * (2 * ST + 2 + a); };
     const uint32_t drain_bar = bars + 8u * (2 * ST + 4);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + ST * stage_bytes<SA, SB>() + 8 * (2 * ST + 5));
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + ST * stage_bytes<SA, SB>() + kEpiBytes + 8 * (2 * ST + 5));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = tc::cluster_rank();                 // CTA of the pair; 0 issues the MMAs
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < ST; ++s) { tc::mbar_init(full_bar(s), kLoadWarps); tc::mbar_init(empty_bar(s), 1); }
-        for (int a = 0; a < 2; ++a) { tc::mbar_init(tfull_bar(a), 1); tc::mbar_init(tempty_bar(a), kEpiWarps); }
+        // full and tempty are used in CTA 0 only, by the warps of both CTAs; empty and tfull are signalled
+        // in both by the MMAs' completion
+        for (int s = 0; s < ST; ++s) { tc::mbar_init(full_bar(s), 2 * kLoadWarps); tc::mbar_init(empty_bar(s), 1); }
+        for (int a = 0; a < 2; ++a) { tc::mbar_init(tfull_bar(a), 1); tc::mbar_init(tempty_bar(a), 2 * kEpiWarps); }
         tc::mbar_init(drain_bar, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (warp == kMmaWarp) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
                      ::"r"(tc::smem_u32(tmem_slot)), "r"(kTmemCols) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc::tc_fence_before();
-    __syncthreads();
+    tc::cluster_sync();
     tc::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     pdl_wait();
@@ -325,70 +349,102 @@ lin_gemm_kernel(const __grid_constant__ Params p)
         // ------------------------------------------------ loaders: global -> bf16 limbs -> shared
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
         const int tid = threadIdx.x;
-        const uint32_t oa = piece_offset<MNA>(tid), ob = piece_offset<MNB>(tid) + LA * kLimbBytes;
-        Cursor<SA, MNA> ca;
-        Cursor<SB, MNB> cb;
-        Raw<SA> ra[kPieces];
-        Raw<SB> rb[kPieces];
+        using CA = Cursor<SA, MNA, kRowsA>;
+        using CB = Cursor<SB, MNB, kRowsB>;
+        constexpr int PA = CA::kPieces, PB = CB::kPieces;
+        const uint32_t oa = CA::offset(tid), ob = CB::offset(tid) + LA * kLimbA;
+        CA ca;
+        CB cb;
+        // Two sets of registers: a step is loaded while the one before the next is converted.
+        struct Set { Raw<SA> a[PA]; Raw<SB> b[PB]; } set0, set1;
         Unit t;
-        int u = blockIdx.x, left = 0;
+        int u = pair, left = 0;
         auto start = [&]() {
             if (!get_unit(p, u, t)) return false;
-            ca.start(p.a, tid, t.m0, t.s0 * BK);
-            cb.start(p.b, tid, t.n0, t.s0 * BK);
+            ca.start(p.a, tid, t.m0 + rank * kRowsA, p.M, t.s0 * BK);
+            cb.start(p.b, tid, t.n0 + rank * kRowsB, p.N, t.s0 * BK);
             left = t.s1 - t.s0;
             return true;
         };
-        bool has = start();
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {   // a unit for every block: the grid is at most the units
-            ca.template load<VEC>(ra[i], p.a, i, p.M, p.K);
-            cb.template load<VEC>(rb[i], p.b, i, p.N, p.K);
-        }
-        int s = 0;
-        uint32_t ph = 0;
-        while (has) {
-            // the cursors move on to the step after this one
-            if (--left > 0) {
+        bool more = start();   // the cursors are at a step that is not loaded (after the last they stay there)
+        auto next = [&]() {
+            if (!more) return;
+            if (left > 1) {
+                --left;
                 ca.advance(p.a);
                 cb.advance(p.b);
             } else {
-                u += gridDim.x;
-                has = start();
+                u += pairs;
+                more = start();
             }
-            if (!tc::mbar_wait(empty_bar(s), ph ^ 1u, abort_flag)) break;
-            uint8_t* sm = gbase + s * stage_bytes<SA, SB>();
-            const int k_end = has ? p.K : 0;
+        };
+        auto fill = [&](Set& r) {
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-                const Raw<SA> va = ra[i];
-                const Raw<SB> vb = rb[i];
-                ca.template load<VEC>(ra[i], p.a, i, p.M, k_end);
-                cb.template load<VEC>(rb[i], p.b, i, p.N, k_end);
-                piece_store<SA>(va, sm + oa + i * (Cursor<SA, MNA>::kRows * 128));
-                piece_store<SB>(vb, sm + ob + i * (Cursor<SB, MNB>::kRows * 128));
+            for (int i = 0; i < PA; ++i) ca.template load<VEC>(r.a[i], p.a, i, p.K);
+#pragma unroll
+            for (int i = 0; i < PB; ++i) cb.template load<VEC>(r.b[i], p.b, i, p.K);
+        };
+        int s = 0;
+        uint32_t ph = 0;
+        // Converts and stores the step in `r` and loads the one at the cursors into the same registers,
+        // piece by piece.  ALL: that one lies inside k: plain loads.
+        auto body = [&](Set& r, auto all) {
+            constexpr bool ALL = decltype(all)::value;
+            uint8_t* sm = gbase + s * stage_bytes<SA, SB>();
+#pragma unroll
+            for (int i = 0; i < PA; ++i) {
+                piece_store<SA, kLimbA>(r.a[i], sm + oa + i * (CA::kRows * 128));
+                if (ALL) ca.load_all(r.a[i], p.a, i);
+                else ca.template load<VEC>(r.a[i], p.a, i, p.K);
             }
+#pragma unroll
+            for (int i = 0; i < PB; ++i) {
+                piece_store<SB, kLimbB>(r.b[i], sm + ob + i * (CB::kRows * 128));
+                if (ALL) cb.load_all(r.b[i], p.b, i);
+                else cb.template load<VEC>(r.b[i], p.b, i, p.K);
+            }
+        };
+        auto process = [&](Set& r) {
+            if (!tc::mbar_wait(empty_bar(s), ph ^ 1u, abort_flag)) return false;
+            if (VEC && (t.s1 - left + 1) * BK <= p.K) body(r, std::true_type());
+            else body(r, std::false_type());
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(full_bar(s));
+            if (lane == 0) tc::mbar_arrive_cluster(full_bar(s), 0);
             if (++s == ST) { s = 0; ph ^= 1u; }
+            return true;
+        };
+        fill(set0);
+        next();
+        fill(set1);
+        bool v1 = more;
+        next();
+        while (true) {
+            const bool v0 = more;
+            if (!process(set0)) break;
+            next();
+            if (!v1) break;
+            v1 = more;
+            if (!process(set1)) break;
+            next();
+            if (!v0) break;
         }
     } else if (warp < kEpiWarp0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
-        if (warp == kMmaWarp) {
+        if (warp == kMmaWarp && rank == 0) {
             // -------------------------------------------- MMA issuer.  The whole warp walks the
             // steps, so that descriptors stay in uniform registers; one elected lane issues.
             // The descriptors of a stage differ from the first stage's in the address field alone.
             const bool leader = tc::elect_one();
+            constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((MNA ? 1u : 0u) << 15) |
+                                       ((MNB ? 1u : 0u) << 16) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
             const uint64_t da = MNA ? mn_desc(base) : tc::sw128_desc(base);
-            const uint64_t db = MNB ? mn_desc(base + LA * kLimbBytes) : tc::sw128_desc(base + LA * kLimbBytes);
+            const uint64_t db = MNB ? mn_desc(base + LA * kLimbA) : tc::sw128_desc(base + LA * kLimbA);
             int s = 0, buf = 0;
             uint32_t ph = 0, bph = 0;
             bool ok = true, issued = false;
             Unit t;
-            for (int u = blockIdx.x; ok && get_unit(p, u, t); u += gridDim.x) {
-                const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((MNA ? 1u : 0u) << 15) |
-                                       ((MNB ? 1u : 0u) << 16) | ((uint32_t)(t.nt >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+            for (int u = pair; ok && get_unit(p, u, t); u += pairs) {
                 int at = 0;
                 for (int step = t.s0; step < t.s1; ++step) {
                     const uint32_t d0 = tmem_base + (uint32_t)(buf * ACC * BN);
@@ -412,24 +468,24 @@ lin_gemm_kernel(const __grid_constant__ Params p)
 #pragma unroll
                                 for (int j = 0; j < LB; ++j) {
                                     if (i + j >= (LA > LB ? LA : LB)) continue;
-                                    const uint64_t ad = sa + (uint32_t)(i * (kLimbBytes >> 4) + kk * KA);
-                                    const uint64_t bd = sb + (uint32_t)(j * (kLimbBytes >> 4) + kk * KB);
+                                    const uint64_t ad = sa + (uint32_t)(i * (kLimbA >> 4) + kk * KA);
+                                    const uint64_t bd = sb + (uint32_t)(j * (kLimbB >> 4) + kk * KB);
                                     const bool add = kk > 0 || at > 0;
                                     if (i + j == 0) {
-                                        tc::tc_mma_f16(d0, ad, bd, idesc, add);
+                                        tc::tc_mma_f16_pair(d0, ad, bd, idesc, add);
                                     } else {
-                                        tc::tc_mma_f16(d0 + BN, ad, bd, idesc, add || low);
+                                        tc::tc_mma_f16_pair(d0 + BN, ad, bd, idesc, add || low);
                                         low = true;
                                     }
                                 }
                         }
-                        tc::tc_commit(empty_bar(s));
+                        tc::tc_commit_pair(empty_bar(s));
                     }
                     issued = true;
                     __syncwarp();
                     if (++s == ST) { s = 0; ph ^= 1u; }
                     if (++at == kChain || step + 1 == t.s1) {
-                        if (leader) tc::tc_commit(tfull_bar(buf));
+                        if (leader) tc::tc_commit_pair(tfull_bar(buf));
                         __syncwarp();
                         at = 0;
                         if (++buf == 2) { buf = 0; bph ^= 1u; }
@@ -437,7 +493,7 @@ lin_gemm_kernel(const __grid_constant__ Params p)
                 }
             }
             if (!ok && issued && leader) {
-                tc::tc_commit(drain_bar);   // completes when every MMA issued so far has finished
+                tc::tc_commit_pair(drain_bar);   // completes when every MMA issued so far has finished
                 const unsigned long long t0 = tc::globaltimer();
                 while (!tc::mbar_try_wait(drain_bar, 0) && tc::globaltimer() - t0 < tc::kWaitLimitNs) {}
             }
@@ -452,62 +508,70 @@ lin_gemm_kernel(const __grid_constant__ Params p)
         uint32_t bph = 0;
         bool ok = true;
         Unit t;
-        for (int u = blockIdx.x; get_unit(p, u, t); u += gridDim.x) {
+        float* buf32 = epi_buf + (warp - kEpiWarp0) * (32 * kStagePitch);
+        for (int u = pair; get_unit(p, u, t); u += pairs) {
             float sum[BN / 2];
 #pragma unroll
             for (int j = 0; j < BN / 2; ++j) sum[j] = 0.f;
-            const bool mine = 64 * half < t.nt;            // a 64-wide tile leaves the other half idle
             for (int c = t.s0; c < t.s1; c += kChain) {
                 if (ok) ok = tc::mbar_wait(tfull_bar(buf), bph, abort_flag);
                 if (!ok) break;
                 tc::tc_fence_after();
-                if (mine) {
-                    const uint32_t d0 = tmem_base + ((uint32_t)lb << 16) + (uint32_t)(buf * ACC * BN + 64 * half);
+                const uint32_t d0 = tmem_base + ((uint32_t)lb << 16) + (uint32_t)(buf * ACC * BN + 64 * half);
 #pragma unroll
-                    for (int a = ACC - 1; a >= 0; --a)     // the small products first
+                for (int a = ACC - 1; a >= 0; --a)     // the small products first
 #pragma unroll
-                        for (int h = 0; h < BN / 2; h += 16) {   // 16 at a time: 64 sums stay in registers
-                            float v[16];
-                            tc::tmem_ld16(d0 + a * BN + h, v);
+                    for (int h = 0; h < BN / 2; h += 16) {   // 16 at a time: 64 sums stay in registers
+                        float v[16];
+                        tc::tmem_ld16(d0 + a * BN + h, v);
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) sum[h + j] += v[j];
-                        }
-                }
+                        for (int j = 0; j < 16; ++j) sum[h + j] += v[j];
+                    }
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(tempty_bar(buf));
+                if (lane == 0) tc::mbar_arrive_cluster(tempty_bar(buf), 0);
                 if (++buf == 2) { buf = 0; bph ^= 1u; }
             }
-            const int m = t.m0 + lb + lane, n0 = t.n0 + 64 * half;
-            if (mine && m < p.M) {
-                float* out = p.out + t.slice * p.slice;
+            if (!ok)
 #pragma unroll
-                for (int j = 0; j < BN / 2; j += 8) {
-                    const int n = n0 + j;
-                    if (n < p.N) {
-                        if (!ok)
+                for (int j = 0; j < BN / 2; ++j) sum[j] = __uint_as_float(0x7fffffffu);
+            // 32 x 32 sub-tiles through shared memory (lane = row in, lane = 4 columns out), so that a
+            // store instruction writes four rows' 128 bytes
+            const int m0 = t.m0 + rank * kRowsA + lb, rows = min(32, p.M - m0);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) sum[j + i] = __uint_as_float(0x7fffffffu);
-                        const int part = n / p.cp, at = n - part * p.cp;
-                        if (at + 8 <= p.cp || part == (p.N - 1) / p.cp) {
-                            store8(out + ((long long)part * p.M + m) * p.cp + at, sum + j, min(8, p.N - n));
-                        } else {   // the eight columns belong to more than one part
+            for (int h = 0; h < 2; ++h) {
+                const int n = t.n0 + 64 * half + 32 * h + 4 * (lane & 7);
+                __syncwarp();
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                if (n + i < p.N)
-                                    out[((long long)((n + i) / p.cp) * p.M + m) * p.cp + (n + i) % p.cp] = sum[j + i];
-                        }
+                for (int j = 0; j < 32; ++j) buf32[lane * kStagePitch + j] = sum[32 * h + j];
+                __syncwarp();
+                if (n >= p.N) continue;
+                const int part = n / p.cp, at = n - part * p.cp;
+                float* out = p.out + t.slice * p.slice + ((long long)part * p.M + m0) * p.cp + at;
+                const bool whole = at + 4 <= p.cp && n + 4 <= p.N && (p.cp & 3) == 0 &&
+                                   (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+                for (int r = lane >> 3; r < rows; r += 4) {
+                    const float* v = buf32 + r * kStagePitch + 4 * (lane & 7);
+                    if (whole) {
+                        *reinterpret_cast<float4*>(out + (long long)r * p.cp) = make_float4(v[0], v[1], v[2], v[3]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)   // the four columns may belong to more than one part
+                            if (n + i < p.N)
+                                p.out[t.slice * p.slice + ((long long)((n + i) / p.cp) * p.M + m0 + r) * p.cp +
+                                      (n + i) % p.cp] = v[i];
                     }
                 }
             }
         }
     }
+    __syncwarp();
     tc::tc_fence_before();
-    __syncthreads();
+    tc::cluster_sync();   // neither CTA leaves while the other may signal or read it
     if (warp == kMmaWarp) {
         __syncwarp();
         tc::tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols) : "memory");
     }
     pdl_launch_dependents();
 }

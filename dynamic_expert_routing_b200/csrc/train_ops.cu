@@ -315,12 +315,12 @@ static int num_sms()
     return n;
 }
 
-// Slices of k: as many as fill the SMs, each of at least kChain steps.
+// Slices of k: as many as fill the pairs of SMs, each of at least kChain steps.
 static void plan_slices(lin::Params& p, int sms)
 {
     const long long tiles = (long long)p.m_tiles * p.n_tiles;
     const long long most = std::max(1LL, ceil_div(p.k_steps, lin::kChain));
-    const long long want = std::min(most, std::max(1LL, sms / tiles));
+    const long long want = std::min(most, std::max(1LL, sms / 2 / tiles));
     p.split_steps = (int)ceil_div(p.k_steps, want);
     p.units = (int)(tiles * ceil_div(p.k_steps, p.split_steps));
 }
@@ -357,7 +357,7 @@ static cudaError_t launch_lin_vec(const lin::Params& p, int sms, cudaStream_t st
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ULL << dev, std::memory_order_relaxed);
     }
-    return launch_free(kernel, dim3((unsigned)std::min(p.units, sms)), dim3(lin::kThreads), smem, st, p);
+    return launch_free(kernel, dim3(2 * (unsigned)std::min(p.units, std::max(1, sms / 2))), dim3(lin::kThreads), smem, st, p);
 }
 
 template <int SA, bool MNA, int SB, bool MNB>
