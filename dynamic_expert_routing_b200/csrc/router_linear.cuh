@@ -24,7 +24,8 @@
 // this one's.  One warp of the first CTA issues the MMAs of both; 8 warps in each drain its rows'
 // accumulators from TMEM (two sets, so that a drain overlaps the next steps) and store.  The grid is
 // persistent; when the tiles are fewer than the CTA pairs, k is cut into slices whose partial tiles
-// lin_reduce_kernel adds in order.
+// lin_reduce_kernel adds in order.  Where k is short (dx: k = c), a pair converts its rows of A once, keeps
+// them in shared memory and walks a range of n with B alone in the ring.
 // Every wait is bounded: when one runs out, the kernel's outputs are set to NaN.
 #pragma once
 #include <type_traits>
@@ -62,9 +63,21 @@ template <int SA, int SB> __host__ __device__ constexpr int stages()
     return n < kMaxStages ? n : kMaxStages;
 }
 template <int SA, int SB> __host__ __device__ constexpr int accs() { return limbs(SA) * limbs(SB) > 1 ? 2 : 1; }
+constexpr int kSmemExtra = kEpiBytes + 1024 /* alignment */ + 256 /* barriers */;
 template <int SA, int SB> __host__ __device__ constexpr int smem_bytes()
 {
-    return stages<SA, SB>() * stage_bytes<SA, SB>() + kEpiBytes + 1024 /* alignment */ + 256 /* barriers */;
+    return stages<SA, SB>() * stage_bytes<SA, SB>() + kSmemExtra;
+}
+// A resident: all k steps of A's share stay in shared memory while the pair walks a range of n, and the
+// ring holds B alone.
+template <int SB> __host__ __device__ constexpr int res_stages() { return limbs(SB) > 1 ? 2 : 4; }
+template <int SA, int SB> __host__ __device__ constexpr int res_steps()   // the most k steps that fit
+{
+    return (kSmemLimit - kSmemExtra - res_stages<SB>() * limbs(SB) * kLimbB) / (limbs(SA) * kLimbA);
+}
+template <int SA, int SB> __host__ __device__ constexpr int res_bytes(int k_steps)
+{
+    return k_steps * limbs(SA) * kLimbA + res_stages<SB>() * limbs(SB) * kLimbB + kSmemExtra;
 }
 
 struct Operand {
@@ -78,8 +91,10 @@ struct Params {
     Operand a, b;
     int M, N, K;
     int m_tiles, n_tiles, k_steps;
-    int split_steps;        // k steps per unit
-    int units;              // slices * m_tiles * n_tiles
+    // Work units of a CTA pair: a tile over a slice of k (split_steps steps), or, with A resident, the
+    // tiles of one m over a range of n (range tiles; k is not cut).
+    int split_steps, range, ranges;
+    int units;
     // Element (m, n) of slice s is at out + s * slice + ((n / cp) * M + m) * cp + n % cp.
     float* out;
     long long slice;
@@ -215,17 +230,20 @@ __device__ __forceinline__ void raw_limbs(const Raw<SRC_F32>& r, uint4* o)
 }
 
 // ---------------------------------------------------------------- units and steps
-struct Unit { int m0, n0, slice, s0, s1; };
+struct Unit { int m0, nt, nt1, slice, s0, s1; };
 
+template <bool RES>
 __device__ __forceinline__ bool get_unit(const Params& p, int u, Unit& t)
 {
     if (u >= p.units) return false;
-    const int nt = u % p.n_tiles, r = u / p.n_tiles;
-    t.n0 = nt * BN;
-    t.m0 = (r % p.m_tiles) * BM;
-    t.slice = r / p.m_tiles;
-    t.s0 = t.slice * p.split_steps;
-    t.s1 = min(p.k_steps, t.s0 + p.split_steps);
+    const int width = RES ? p.ranges : p.n_tiles;
+    const int c = u % width, r = u / width;
+    t.nt = RES ? c * p.range : c;
+    t.nt1 = RES ? min(p.n_tiles, t.nt + p.range) : c + 1;
+    t.m0 = (RES ? r : r % p.m_tiles) * BM;
+    t.slice = RES ? 0 : r / p.m_tiles;
+    t.s0 = RES ? 0 : t.slice * p.split_steps;
+    t.s1 = RES ? p.k_steps : min(p.k_steps, t.s0 + p.split_steps);
     return true;
 }
 
@@ -238,9 +256,11 @@ template <int SRC, bool MN, int ROWS> struct Cursor {
     static constexpr int kChunks = MN ? ROWS / 8 : 8;
     static constexpr int kRows = 32 * kLoadWarps / kChunks;        // rows of a block between pieces
     static constexpr int kPieces = (MN ? BK : ROWS) / kRows;
+    static_assert(kPieces <= 2, "one distance between pieces");
     const char* p;           // piece 0 of the current step
     const uint8_t* sc;
-    int k;                   // its first k
+    long long next;          // bytes from piece 0 to piece 1
+    int k;                   // the first k of piece 0
     int n;                   // MN-major: values that the chunk has (<= 0: none);  K-major: rows from piece 0 on
     int off;                 // distance of a chunk's second 16 bytes
     __device__ __forceinline__ void start(const Operand& o, int tid, int x0, int xs, int k0)
@@ -249,12 +269,12 @@ template <int SRC, bool MN, int ROWS> struct Cursor {
         int x = x0 + (MN ? 8 * chunk : row);
         k = k0 + (MN ? row : 8 * chunk);
         n = xs - x;
-        off = !MN || n > 4 ? 16 : 0;
-        if (n <= 0) { x = MN ? (xs - 1) & ~7 : xs - 1; off = 0; }   // a place that can be read
+        if (n <= 0) x = MN ? (xs - 1) & ~7 : xs - 1;   // a place that can be read
+        off = MN && n <= 4 ? 0 : 16;
         const long long r = MN ? k : x, c = MN ? x : k;
         p = static_cast<const char*>(o.p) + (r * o.ld + c) * ES;
+        next = MN || kRows < n ? kRows * o.ld * ES : 0;
         if (SRC == SRC_CKPT) sc = o.scale + r * (o.ld >> 5) + (c >> 5);
-        if (!MN && n <= 0) off = 16;
     }
     __device__ __forceinline__ void advance(const Operand& o)
     {
@@ -263,15 +283,14 @@ template <int SRC, bool MN, int ROWS> struct Cursor {
         if (SRC == SRC_CKPT) sc += MN ? BK * (o.ld >> 5) : BK >> 5;
     }
     // Piece i where the whole step lies inside k.
-    __device__ __forceinline__ void load_all(Raw<SRC>& r, const Operand& o, int i) const
+    __device__ __forceinline__ void load_all(Raw<SRC>& r, int i) const
     {
-        const long long d = MN || i * kRows < n ? i * kRows : 0;
-        raw_load_all(r, p + d * o.ld * ES, sc + d * (o.ld >> 5), off);
+        raw_load_all(r, p + (i ? next : 0), SRC == SRC_CKPT ? sc + (i ? (next >> 5) : 0) : nullptr, off);
     }
-    template <bool VEC> __device__ __forceinline__ void load(Raw<SRC>& r, const Operand& o, int i, int K) const
+    template <bool VEC> __device__ __forceinline__ void load(Raw<SRC>& r, int i, int K) const
     {
         const int ki = MN ? k + i * kRows : k, have = MN ? n : n - i * kRows;
-        raw_load<VEC>(r, p + i * kRows * o.ld * ES, sc + i * kRows * (o.ld >> 5),
+        raw_load<VEC>(r, p + (i ? next : 0), SRC == SRC_CKPT ? sc + (i ? (next >> 5) : 0) : nullptr,
                       have > 0 && ki < K ? (MN ? n : K - k) : 0);
     }
     // Byte offset of piece 0 in a limb's swizzled tile; piece i is kRows * 128 bytes on (a multiple of
@@ -300,25 +319,29 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t saddr)
     return tc::sw128_desc(saddr) - ((uint64_t)1 << 16) + ((uint64_t)((BK * 128) >> 4) << 16);
 }
 
-template <int SA, bool MNA, int SB, bool MNB, bool VEC>
+template <int SA, bool MNA, int SB, bool MNB, bool VEC, bool RES>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 lin_gemm_kernel(const __grid_constant__ Params p)
 {
-    constexpr int LA = limbs(SA), LB = limbs(SB), ST = stages<SA, SB>(), ACC = accs<SA, SB>();
+    constexpr int LA = limbs(SA), LB = limbs(SB), ST = RES ? res_stages<SB>() : stages<SA, SB>(), ACC = accs<SA, SB>();
+    constexpr int kStage = RES ? LB * kLimbB : stage_bytes<SA, SB>();   // bytes of a ring stage
     constexpr int kTmemCols = 512;   // 2 sets of ACC accumulators of BN columns, at the same place in both CTAs
     static_assert(2 * ACC * BN <= kTmemCols, "accumulators");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = tc::smem_u32(smem_raw);
     const uint32_t base = (raw_addr + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - raw_addr);
-    float* epi_buf = reinterpret_cast<float*>(gbase + ST * stage_bytes<SA, SB>());
-    const uint32_t bars = base + ST * stage_bytes<SA, SB>() + kEpiBytes;
+    const uint32_t ring = RES ? p.k_steps * (LA * kLimbA) : 0;           // where the ring starts, behind a resident A
+    const uint32_t bpart = RES ? 0 : LA * kLimbA;                        // B's place in a stage
+    float* epi_buf = reinterpret_cast<float*>(gbase + ring + ST * kStage);
+    const uint32_t bars = base + ring + ST * kStage + kEpiBytes;
     auto full_bar = [&](int s) { return bars + 8u * s; };
     auto empty_bar = [&](int s) { return bars + 8u * (ST + s); };
     auto tfull_bar = [&](int a) { return bars + 8u * (2 * ST + a); };
     auto tempty_bar = [&](int a) { return bars + 8u * (2 * ST + 2 + a); };
     const uint32_t drain_bar = bars + 8u * (2 * ST + 4);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + ST * stage_bytes<SA, SB>() + kEpiBytes + 8 * (2 * ST + 5));
+    const uint32_t afree_bar = bars + 8u * (2 * ST + 5);   // RES: the MMAs on the resident A have finished
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + (bars - base) + 8 * (2 * ST + 6));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = tc::cluster_rank();                 // CTA of the pair; 0 issues the MMAs
@@ -330,6 +353,7 @@ lin_gemm_kernel(const __grid_constant__ Params p)
         for (int s = 0; s < ST; ++s) { tc::mbar_init(full_bar(s), 2 * kLoadWarps); tc::mbar_init(empty_bar(s), 1); }
         for (int a = 0; a < 2; ++a) { tc::mbar_init(tfull_bar(a), 1); tc::mbar_init(tempty_bar(a), 2 * kEpiWarps); }
         tc::mbar_init(drain_bar, 1);
+        tc::mbar_init(afree_bar, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -352,37 +376,41 @@ lin_gemm_kernel(const __grid_constant__ Params p)
         using CA = Cursor<SA, MNA, kRowsA>;
         using CB = Cursor<SB, MNB, kRowsB>;
         constexpr int PA = CA::kPieces, PB = CB::kPieces;
-        const uint32_t oa = CA::offset(tid), ob = CB::offset(tid) + LA * kLimbA;
+        const uint32_t oa = CA::offset(tid), ob = CB::offset(tid) + ring + bpart;
         CA ca;
         CB cb;
         // Two sets of registers: a step is loaded while the one before the next is converted.
-        struct Set { Raw<SA> a[PA]; Raw<SB> b[PB]; } set0, set1;
-        Unit t;
+        struct Set { Raw<SA> a[RES ? 1 : PA]; Raw<SB> b[PB]; } set0, set1;
+        Unit t = {};
         int u = pair, left = 0;
-        auto start = [&]() {
-            if (!get_unit(p, u, t)) return false;
-            ca.start(p.a, tid, t.m0 + rank * kRowsA, p.M, t.s0 * BK);
-            cb.start(p.b, tid, t.n0 + rank * kRowsB, p.N, t.s0 * BK);
+        auto start_tile = [&]() {
+            if (!RES) ca.start(p.a, tid, t.m0 + rank * kRowsA, p.M, t.s0 * BK);
+            cb.start(p.b, tid, t.nt * BN + rank * kRowsB, p.N, t.s0 * BK);
             left = t.s1 - t.s0;
-            return true;
         };
-        bool more = start();   // the cursors are at a step that is not loaded (after the last they stay there)
+        bool more = get_unit<RES>(p, u, t);   // the cursors are at a step that is not loaded (or, at the end, at the last)
+        start_tile();
         auto next = [&]() {
             if (!more) return;
             if (left > 1) {
                 --left;
-                ca.advance(p.a);
+                if (!RES) ca.advance(p.a);
                 cb.advance(p.b);
+            } else if (RES && t.nt + 1 < t.nt1) {
+                ++t.nt;
+                start_tile();
             } else {
                 u += pairs;
-                more = start();
+                more = get_unit<RES>(p, u, t);
+                if (more) start_tile();
             }
         };
         auto fill = [&](Set& r) {
+            if (!RES)
 #pragma unroll
-            for (int i = 0; i < PA; ++i) ca.template load<VEC>(r.a[i], p.a, i, p.K);
+                for (int i = 0; i < PA; ++i) ca.template load<VEC>(r.a[RES ? 0 : i], i, p.K);
 #pragma unroll
-            for (int i = 0; i < PB; ++i) cb.template load<VEC>(r.b[i], p.b, i, p.K);
+            for (int i = 0; i < PB; ++i) cb.template load<VEC>(r.b[i], i, p.K);
         };
         int s = 0;
         uint32_t ph = 0;
@@ -390,21 +418,44 @@ lin_gemm_kernel(const __grid_constant__ Params p)
         // piece by piece.  ALL: that one lies inside k: plain loads.
         auto body = [&](Set& r, auto all) {
             constexpr bool ALL = decltype(all)::value;
-            uint8_t* sm = gbase + s * stage_bytes<SA, SB>();
+            uint8_t* sm = gbase + s * kStage;
+            if (!RES)
 #pragma unroll
-            for (int i = 0; i < PA; ++i) {
-                piece_store<SA, kLimbA>(r.a[i], sm + oa + i * (CA::kRows * 128));
-                if (ALL) ca.load_all(r.a[i], p.a, i);
-                else ca.template load<VEC>(r.a[i], p.a, i, p.K);
-            }
+                for (int i = 0; i < PA; ++i) {
+                    Raw<SA>& v = r.a[RES ? 0 : i];
+                    piece_store<SA, kLimbA>(v, sm + oa + i * (CA::kRows * 128));
+                    if (ALL) ca.load_all(v, i);
+                    else ca.template load<VEC>(v, i, p.K);
+                }
 #pragma unroll
             for (int i = 0; i < PB; ++i) {
                 piece_store<SB, kLimbB>(r.b[i], sm + ob + i * (CB::kRows * 128));
-                if (ALL) cb.load_all(r.b[i], p.b, i);
-                else cb.template load<VEC>(r.b[i], p.b, i, p.K);
+                if (ALL) cb.load_all(r.b[i], i);
+                else cb.template load<VEC>(r.b[i], i, p.K);
             }
         };
+        // RES: the unit whose steps are being stored, its steps to come, and the units before it
+        int cu = pair, rest = 0, units = 0;
         auto process = [&](Set& r) {
+            if (RES && rest == 0) {
+                Unit c;
+                get_unit<RES>(p, cu, c);
+                if (units > 0 && !tc::mbar_wait(afree_bar, (units - 1) & 1, abort_flag)) return false;
+                ca.start(p.a, tid, c.m0 + rank * kRowsA, p.M, 0);
+                for (int k = 0; k < p.k_steps; ++k) {
+                    Raw<SA> v[PA];
+#pragma unroll
+                    for (int i = 0; i < PA; ++i) ca.template load<VEC>(v[i], i, p.K);
+#pragma unroll
+                    for (int i = 0; i < PA; ++i)
+                        piece_store<SA, kLimbA>(v[i], gbase + k * (LA * kLimbA) + oa + i * (CA::kRows * 128));
+                    ca.advance(p.a);
+                }
+                rest = (c.nt1 - c.nt) * p.k_steps;
+                cu += pairs;
+                ++units;
+            }
+            if (RES) --rest;
             if (!tc::mbar_wait(empty_bar(s), ph ^ 1u, abort_flag)) return false;
             if (VEC && (t.s1 - left + 1) * BK <= p.K) body(r, std::true_type());
             else body(r, std::false_type());
@@ -439,22 +490,23 @@ lin_gemm_kernel(const __grid_constant__ Params p)
             constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((MNA ? 1u : 0u) << 15) |
                                        ((MNB ? 1u : 0u) << 16) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
             const uint64_t da = MNA ? mn_desc(base) : tc::sw128_desc(base);
-            const uint64_t db = MNB ? mn_desc(base + LA * kLimbA) : tc::sw128_desc(base + LA * kLimbA);
+            const uint64_t db = MNB ? mn_desc(base + ring + bpart) : tc::sw128_desc(base + ring + bpart);
             int s = 0, buf = 0;
             uint32_t ph = 0, bph = 0;
             bool ok = true, issued = false;
             Unit t;
-            for (int u = pair; ok && get_unit(p, u, t); u += pairs) {
+            for (int u = pair; ok && get_unit<RES>(p, u, t); u += pairs) {
                 int at = 0;
-                for (int step = t.s0; step < t.s1; ++step) {
+                const int steps = t.s1 - t.s0, total = RES ? (t.nt1 - t.nt) * steps : steps;
+                for (int i = 0, step = t.s0; i < total; ++i) {
                     const uint32_t d0 = tmem_base + (uint32_t)(buf * ACC * BN);
                     if (at == 0) {
                         if (!tc::mbar_wait(tempty_bar(buf), bph ^ 1u, abort_flag)) { ok = false; break; }
                     }
                     if (!tc::mbar_wait(full_bar(s), ph, abort_flag)) { ok = false; break; }
                     tc::tc_fence_after();
-                    const uint64_t sa = da + (uint32_t)(s * (stage_bytes<SA, SB>() >> 4));
-                    const uint64_t sb = db + (uint32_t)(s * (stage_bytes<SA, SB>() >> 4));
+                    const uint64_t sa = da + (uint32_t)(RES ? step * (LA * kLimbA >> 4) : s * (kStage >> 4));
+                    const uint64_t sb = db + (uint32_t)(s * (kStage >> 4));
                     const int k_left = p.K - step * BK;
                     if (leader) {
 #pragma unroll
@@ -484,12 +536,17 @@ lin_gemm_kernel(const __grid_constant__ Params p)
                     issued = true;
                     __syncwarp();
                     if (++s == ST) { s = 0; ph ^= 1u; }
-                    if (++at == kChain || step + 1 == t.s1) {
-                        if (leader) tc::tc_commit_pair(tfull_bar(buf));
+                    const bool last = ++step == t.s1;      // of a tile
+                    if (++at == kChain || last) {
+                        if (leader) {
+                            tc::tc_commit_pair(tfull_bar(buf));
+                            if (RES && i + 1 == total) tc::tc_commit_pair(afree_bar);
+                        }
                         __syncwarp();
                         at = 0;
                         if (++buf == 2) { buf = 0; bph ^= 1u; }
                     }
+                    if (last) step = t.s0;
                 }
             }
             if (!ok && issued && leader) {
@@ -509,7 +566,8 @@ lin_gemm_kernel(const __grid_constant__ Params p)
         bool ok = true;
         Unit t;
         float* buf32 = epi_buf + (warp - kEpiWarp0) * (32 * kStagePitch);
-        for (int u = pair; get_unit(p, u, t); u += pairs) {
+        for (int u = pair; get_unit<RES>(p, u, t); u += pairs)
+        for (int nt = t.nt; nt < t.nt1; ++nt) {
             float sum[BN / 2];
 #pragma unroll
             for (int j = 0; j < BN / 2; ++j) sum[j] = 0.f;
@@ -540,7 +598,7 @@ lin_gemm_kernel(const __grid_constant__ Params p)
             const int m0 = t.m0 + rank * kRowsA + lb, rows = min(32, p.M - m0);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int n = t.n0 + 64 * half + 32 * h + 4 * (lane & 7);
+                const int n = nt * BN + 64 * half + 32 * h + 4 * (lane & 7);
                 __syncwarp();
 #pragma unroll
                 for (int j = 0; j < 32; ++j) buf32[lane * kStagePitch + j] = sum[32 * h + j];
@@ -550,7 +608,9 @@ lin_gemm_kernel(const __grid_constant__ Params p)
                 float* out = p.out + t.slice * p.slice + ((long long)part * p.M + m0) * p.cp + at;
                 const bool whole = at + 4 <= p.cp && n + 4 <= p.N && (p.cp & 3) == 0 &&
                                    (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-                for (int r = lane >> 3; r < rows; r += 4) {
+#pragma unroll
+                for (int r = lane >> 3; r < 32; r += 4) {
+                    if (r >= rows) break;
                     const float* v = buf32 + r * kStagePitch + 4 * (lane & 7);
                     if (whole) {
                         *reinterpret_cast<float4*>(out + (long long)r * p.cp) = make_float4(v[0], v[1], v[2], v[3]);

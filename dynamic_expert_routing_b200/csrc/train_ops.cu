@@ -316,11 +316,11 @@ static int num_sms()
 }
 
 // Slices of k: as many as fill the pairs of SMs, each of at least kChain steps.
-static void plan_slices(lin::Params& p, int sms)
+static void plan_slices(lin::Params& p, int pairs)
 {
     const long long tiles = (long long)p.m_tiles * p.n_tiles;
     const long long most = std::max(1LL, ceil_div(p.k_steps, lin::kChain));
-    const long long want = std::min(most, std::max(1LL, sms / 2 / tiles));
+    const long long want = std::min(most, std::max(1LL, pairs / tiles));
     p.split_steps = (int)ceil_div(p.k_steps, want);
     p.units = (int)(tiles * ceil_div(p.k_steps, p.split_steps));
 }
@@ -343,28 +343,60 @@ static lin::Operand operand(const void* x, int dtype, long long ld, long long co
     return {x, nullptr, ld, !misaligned(x, 16) && ld % v == 0 && cols % v == 0};
 }
 
-template <int SA, bool MNA, int SB, bool MNB, bool VEC>
-static cudaError_t launch_lin_vec(const lin::Params& p, int sms, cudaStream_t st)
+// Ranges of n per m tile for a resident A: each pair's time is about the tiles it walks plus one for
+// converting A per unit; the fewest rounds times that wins.
+static void plan_ranges(lin::Params& p, int pairs)
 {
-    auto kernel = lin::lin_gemm_kernel<SA, MNA, SB, MNB, VEC>;
-    constexpr int smem = lin::smem_bytes<SA, SB>();
+    long long best = -1;
+    for (int r = 1; r <= p.n_tiles && r <= 4 * pairs; ++r) {
+        const int len = (int)ceil_div(p.n_tiles, r), ranges = (int)ceil_div(p.n_tiles, len);
+        const long long cost = ceil_div((long long)p.m_tiles * ranges, pairs) * (len + 1);
+        if (best < 0 || cost < best) {
+            best = cost;
+            p.range = len;
+            p.ranges = ranges;
+            p.units = p.m_tiles * ranges;
+        }
+    }
+}
+
+template <int SA, bool MNA, int SB, bool MNB, bool VEC, bool RES>
+static cudaError_t launch_lin_as(const lin::Params& p, int pairs, cudaStream_t st)
+{
+    auto kernel = lin::lin_gemm_kernel<SA, MNA, SB, MNB, VEC, RES>;
+    const int smem = RES ? lin::res_bytes<SA, SB>(p.k_steps) : lin::smem_bytes<SA, SB>();
     static std::atomic<unsigned long long> ready;   // devices whose attribute is set
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, lin::kSmemLimit);
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ULL << dev, std::memory_order_relaxed);
     }
-    return launch_free(kernel, dim3(2 * (unsigned)std::min(p.units, std::max(1, sms / 2))), dim3(lin::kThreads), smem, st, p);
+    return launch_free(kernel, dim3(2 * (unsigned)std::min(p.units, pairs)), dim3(lin::kThreads), smem, st, p);
 }
 
+// k is not cut (dx).
 template <int SA, bool MNA, int SB, bool MNB>
-static cudaError_t launch_lin(const lin::Params& p, int sms, cudaStream_t st)
+static cudaError_t launch_rows(lin::Params p, int pairs, cudaStream_t st)
 {
-    return p.a.vec && p.b.vec ? launch_lin_vec<SA, MNA, SB, MNB, true>(p, sms, st)
-                              : launch_lin_vec<SA, MNA, SB, MNB, false>(p, sms, st);
+    const bool vec = p.a.vec && p.b.vec;
+    if (p.n_tiles > 1 && p.k_steps <= lin::res_steps<SA, SB>()) {
+        plan_ranges(p, pairs);
+        return vec ? launch_lin_as<SA, MNA, SB, MNB, true, true>(p, pairs, st)
+                   : launch_lin_as<SA, MNA, SB, MNB, false, true>(p, pairs, st);
+    }
+    return vec ? launch_lin_as<SA, MNA, SB, MNB, true, false>(p, pairs, st)
+               : launch_lin_as<SA, MNA, SB, MNB, false, false>(p, pairs, st);
+}
+
+// k may be cut into slices (dW).
+template <int SA, bool MNA, int SB, bool MNB>
+static cudaError_t launch_slices(const lin::Params& p, int pairs, cudaStream_t st)
+{
+    return p.a.vec && p.b.vec ? launch_lin_as<SA, MNA, SB, MNB, true, false>(p, pairs, st)
+                              : launch_lin_as<SA, MNA, SB, MNB, false, false>(p, pairs, st);
 }
 
 // Workspace of the weight gradient: the slices' partial tiles.
@@ -372,7 +404,7 @@ static int weight_ld(int C) { return (C + 7) & ~7; }
 static lin::Params weight_params(int T, int C, int d)
 {
     lin::Params p = lin_params(d, C, T);
-    plan_slices(p, num_sms());
+    plan_slices(p, std::max(1, num_sms() / 2));
     return p;
 }
 static long long weight_bytes(const lin::Params& p)
@@ -424,9 +456,9 @@ beam_status_t beam_router_weight_grad(const int8_t* q, const uint8_t* scale, int
     p.out = need ? static_cast<float*>(workspace) : dw;
     p.slice = (long long)d * ldp;
     p.cp = need ? ldp : cp;
-    const int sms = num_sms();
-    const cudaError_t e = dtype == BEAM_DTYPE_F32 ? launch_lin<lin::SRC_CKPT, true, lin::SRC_F32, true>(p, sms, st)
-                                                  : launch_lin<lin::SRC_CKPT, true, lin::SRC_BF16, true>(p, sms, st);
+    const int pairs = std::max(1, num_sms() / 2);
+    const cudaError_t e = dtype == BEAM_DTYPE_F32 ? launch_slices<lin::SRC_CKPT, true, lin::SRC_F32, true>(p, pairs, st)
+                                                  : launch_slices<lin::SRC_CKPT, true, lin::SRC_BF16, true>(p, pairs, st);
     BEAM_HOST_CUDA(e);
     if (need) {
         const long long n = (long long)d * ceil_div(C, 4);
@@ -451,13 +483,13 @@ beam_status_t beam_router_input_grad(const void* dlogits, int32_t dtype, int64_t
     p.b = operand(w, w_dtype, ld_w, C);
     p.out = dx;
     p.cp = d;
-    const int sms = num_sms();
+    const int pairs = std::max(1, num_sms() / 2);
     const bool g32 = dtype == BEAM_DTYPE_F32, w32 = w_dtype == BEAM_DTYPE_F32;
     const cudaError_t e =
-        g32 ? (w32 ? launch_lin<lin::SRC_F32, false, lin::SRC_F32, false>(p, sms, st)
-                   : launch_lin<lin::SRC_F32, false, lin::SRC_BF16, false>(p, sms, st))
-            : (w32 ? launch_lin<lin::SRC_BF16, false, lin::SRC_F32, false>(p, sms, st)
-                   : launch_lin<lin::SRC_BF16, false, lin::SRC_BF16, false>(p, sms, st));
+        g32 ? (w32 ? launch_rows<lin::SRC_F32, false, lin::SRC_F32, false>(p, pairs, st)
+                   : launch_rows<lin::SRC_F32, false, lin::SRC_BF16, false>(p, pairs, st))
+            : (w32 ? launch_rows<lin::SRC_BF16, false, lin::SRC_F32, false>(p, pairs, st)
+                   : launch_rows<lin::SRC_BF16, false, lin::SRC_BF16, false>(p, pairs, st));
     BEAM_HOST_CUDA(e);
     return BEAM_OK;
 }
