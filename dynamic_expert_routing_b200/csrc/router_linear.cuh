@@ -41,15 +41,16 @@ constexpr int kLimbA = kRowsA * BK * 2, kLimbB = kRowsB * BK * 2;   // bytes of 
 constexpr int kChain = 4;                     // steps added in the tensor cores' accumulator
 // Warpgroups of 4 warps: 4 that load and convert, one whose first warp issues the MMAs, 2 that drain.
 // The kernel is launched with 72 registers a thread (7 x 128 x 72 of the SM's 65536); the
-// epilogue, which keeps 64 sums per thread, takes some from the others: 512 x 64 + 128 x 40 + 256 x 104
+// epilogue, which keeps 64 sums per thread, takes some from the others: 512 x 64 + 128 x 24 + 256 x 112
 // = 64512 registers, the launch's own total.
 constexpr int kLoadWarps = 16, kEpiWarps = 8, kMmaWarp = kLoadWarps, kEpiWarp0 = kLoadWarps + 4;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
-constexpr int kLaunchRegs = 72, kLoadRegs = 64, kMmaRegs = 40, kEpiRegs = 104;
+constexpr int kLaunchRegs = 72, kLoadRegs = 64, kMmaRegs = 24, kEpiRegs = 112;
 static_assert(32 * kLoadWarps * kLoadRegs + 128 * kMmaRegs + 32 * kEpiWarps * kEpiRegs <= kThreads * kLaunchRegs,
               "the register shares must fit the launch's");
 constexpr int kMaxStages = 4;
-constexpr int kStagePitch = 33;               // epilogue staging: 32 x 32 sub-tiles, conflict-free both ways
+constexpr int kStagePitch = 36;               // epilogue staging: 32 x 32 sub-tiles, 16-byte accesses without
+                                              // conflicts both ways
 constexpr int kEpiBytes = kEpiWarps * 32 * kStagePitch * 4;
 constexpr int kSmemLimit = 227 * 1024;
 
@@ -601,26 +602,27 @@ lin_gemm_kernel(const __grid_constant__ Params p)
                 const int n = nt * BN + 64 * half + 32 * h + 4 * (lane & 7);
                 __syncwarp();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) buf32[lane * kStagePitch + j] = sum[32 * h + j];
+                for (int j = 0; j < 32; j += 4)
+                    *reinterpret_cast<float4*>(buf32 + lane * kStagePitch + j) =
+                        make_float4(sum[32 * h + j], sum[32 * h + j + 1], sum[32 * h + j + 2], sum[32 * h + j + 3]);
                 __syncwarp();
                 if (n >= p.N) continue;
                 const int part = n / p.cp, at = n - part * p.cp;
                 float* out = p.out + t.slice * p.slice + ((long long)part * p.M + m0) * p.cp + at;
-                const bool whole = at + 4 <= p.cp && n + 4 <= p.N && (p.cp & 3) == 0 &&
-                                   (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-#pragma unroll
-                for (int r = lane >> 3; r < 32; r += 4) {
-                    if (r >= rows) break;
-                    const float* v = buf32 + r * kStagePitch + 4 * (lane & 7);
-                    if (whole) {
-                        *reinterpret_cast<float4*>(out + (long long)r * p.cp) = make_float4(v[0], v[1], v[2], v[3]);
-                    } else {
+                const float* v = buf32 + 4 * (lane & 7);
+                if (at + 4 <= p.cp && n + 4 <= p.N && (p.cp & 3) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0) {
+                    const int r0 = lane >> 3;
+                    float* o = out + (long long)r0 * p.cp;
+#pragma unroll 4
+                    for (int r = r0; r < rows; r += 4, o += 4 * p.cp)
+                        *reinterpret_cast<float4*>(o) = *reinterpret_cast<const float4*>(v + r * kStagePitch);
+                } else {
+                    for (int r = lane >> 3; r < rows; r += 4)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)   // the four columns may belong to more than one part
                             if (n + i < p.N)
                                 p.out[t.slice * p.slice + ((long long)((n + i) / p.cp) * p.M + m0 + r) * p.cp +
-                                      (n + i) % p.cp] = v[i];
-                    }
+                                      (n + i) % p.cp] = v[r * kStagePitch + i];
                 }
             }
         }
