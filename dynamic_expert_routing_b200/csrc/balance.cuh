@@ -10,24 +10,29 @@
 // Replacing f by f - 1 = (c E - K n) / (K n) leaves that gradient unchanged (sum_j p_tj = 1) and
 // removes the cancellation of two numbers near 1: the numerator is an exact integer.
 //
-// Kernels:
-//   balance_partial_kernel   a CTA takes a fixed run of tokens and writes, for each group that
-//                            the run meets, the sums of p, the counts and the token count.
-//                            Run c and group g meet in slot c + g: along the tokens one of the
-//                            two grows at every step, so the slots are distinct and fewer than
-//                            runs + groups.
-//   balance_reduce_kernel    a CTA per group adds its slots in order and forms f, P and L_g; the
-//                            last CTA to finish (a ticket) takes the mean over the groups.
-//   balance_grad_kernel      a warp per token: the gradient above, and optionally the scattered
-//                            slot gradients of the routing beside it.
+// Kernels (LPR lanes share a row of logits, 8 values each, so that a warp takes 32 / LPR rows at once
+// and few lanes idle whatever E):
+//   balance_partial_kernel   a CTA takes a run of tokens and writes, for each group that the run
+//                            meets, the sums of p, the counts and the token count.  Run c and
+//                            group g meet in slot c + g: along the tokens one of the two grows at
+//                            every step, so the slots are distinct and fewer than runs + groups.
+//                            A batch of one run and one group is finished here, in one launch.
+//   balance_reduce_kernel    a CTA per group and 32 experts adds their slots in order and forms f, P
+//                            and the experts' part of L_g; the last CTA to finish (a ticket) adds the
+//                            parts and takes the mean over the groups.
+//   balance_grad_kernel      the gradient above, and optionally the slot gradients of the routing
+//                            scattered beside it; a warp's rows are put together in shared memory
+//                            and leave as one contiguous piece.
 // All float sums have a fixed order; the atomics count integers or elect the last CTA.
 #pragma once
 #include "common.cuh"
 
 namespace beam {
 
-constexpr int kBalRun = 64;      // tokens per CTA of the first pass
-constexpr int kBalThreads = 256;
+constexpr int kBalThreads = 256, kBalWarps = kBalThreads / 32;
+constexpr int kBalPer = 8;            // logits per lane
+constexpr int kBalRuns = 296;         // most runs of a large batch: two CTAs per SM
+constexpr int kBalReduceThreads = 1024;
 
 // Group bounds [cu[g], cu[g+1]) clamped to the batch; one group [0, T) without cu.
 __device__ __forceinline__ int bal_bound(const int* __restrict__ cu, int g, int T)
@@ -45,223 +50,352 @@ __device__ __forceinline__ int bal_group(const int* __restrict__ cu, int n_seq, 
     return lo;
 }
 
-// softmax of one row held as v[j] = logit lane + 32 j (-inf past E); a row without a logit
-// above -inf has probability 0 everywhere.
-template <int EPL>
-__device__ __forceinline__ void bal_softmax(float* v)
+// The same for the whole block.  Up to kBalCount groups, the threads count the groups that end at or
+// before t: one round trip to memory instead of one per halving (24 groups: 5).
+constexpr int kBalCount = 2048;
+__device__ __forceinline__ int bal_group_block(const int* __restrict__ cu, int n_seq, int t, int* s_cnt)
 {
-    float m = -INFINITY, s = 0.f;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) m = fmaxf(m, v[j]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (m == -INFINITY) {
-        // fmaxf ignores a NaN: only a row of -inf alone is empty
-        float t = 0.f;
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) t += isnan(v[j]) ? v[j] : 0.f;
-        t = warp_sum(t);
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) v[j] = t;
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) { v[j] = expf(v[j] - m); s += v[j]; }
-    s = warp_sum(s);
-    const float inv = 1.0f / s;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) v[j] *= inv;
+    if (n_seq > kBalCount) return bal_group(cu, n_seq, t);
+    if (threadIdx.x == 0) *s_cnt = 0;
+    __syncthreads();
+    int n = 0;
+    for (int i = threadIdx.x; i < n_seq; i += blockDim.x) n += __ldg(cu + i + 1) <= t;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if ((threadIdx.x & 31) == 0 && n) atomicAdd(s_cnt, n);
+    __syncthreads();
+    return *s_cnt;
 }
 
-template <typename T, int EPL>
+// softmax of one row held by LPR lanes as v[j] = logit r + LPR j, r the lane's place in the row (-inf
+// past E); a row without a logit above -inf has probability 0 everywhere.
+template <int LPR>
+__device__ __forceinline__ void bal_softmax(float* v)
+{
+    float m = v[0], s = 0.f, bad = 0.f;
+#pragma unroll
+    for (int j = 1; j < kBalPer; ++j) m = fmaxf(m, v[j]);
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const bool none = m == -INFINITY;   // fmaxf passes over a NaN: such a row has -inf and NaN only
+#pragma unroll
+    for (int j = 0; j < kBalPer; ++j) {
+        if (none) bad += isnan(v[j]) ? v[j] : 0.f;
+        v[j] = none ? 0.f : expf(v[j] - m);
+        s += v[j];
+    }
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        bad += __shfl_xor_sync(0xffffffffu, bad, o);
+    }
+    const float inv = none ? bad : 1.0f / s;
+#pragma unroll
+    for (int j = 0; j < kBalPer; ++j) v[j] = none ? inv : v[j] * inv;
+}
+
+template <typename T, int LPR>
+__device__ __forceinline__ void bal_load(float* v, const T* __restrict__ row, int r, int E, bool on)
+{
+#pragma unroll
+    for (int j = 0; j < kBalPer; ++j) {
+        const int e = r + LPR * j;
+        v[j] = on && e < E ? to_float(row[e]) : -INFINITY;
+    }
+}
+
+// Sum over the block of one value per thread (blockDim a multiple of 32, at most 1024), in a fixed order; in
+// all threads.
+__device__ __forceinline__ float bal_block_sum(float v, float* s_w)
+{
+    v = warp_sum(v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s_w[threadIdx.x >> 5] = v;
+    __syncthreads();
+    const int w = threadIdx.x & 31;
+    return warp_sum(w < (int)(blockDim.x >> 5) ? s_w[w] : 0.f);
+}
+
+// prob, counts and (expert 0) tokens of one group from the sums of a thread's expert (none: e >= E), and
+// the block's share of the group's loss.
+__device__ __forceinline__ float bal_finish(int g, int e, int E, int K, float sum, int cnt, int n,
+                                            float* __restrict__ prob, int* __restrict__ counts,
+                                            int* __restrict__ tokens, float* s_w)
+{
+    float l = 0.f;
+    if (e < E) {
+        const float p = n ? sum / (float)n : 0.f;
+        prob[(long long)g * E + e] = p;
+        counts[(long long)g * E + e] = cnt;
+        if (n) l = p * (float)((double)cnt * E / ((double)K * n));
+    }
+    if (e == 0) tokens[g] = n;
+    return bal_block_sum(l, s_w);
+}
+
+template <typename T, int LPR>
 __global__ void __launch_bounds__(kBalThreads)
-balance_partial_kernel(const T* __restrict__ logits, long long ldl, int n_tok, int E,
+balance_partial_kernel(const T* __restrict__ logits, long long ldl, int n_tok, int E, int run,
                        const int* __restrict__ topk, int K, const uint8_t* __restrict__ valid,
                        const int* __restrict__ cu, int n_seq, float* __restrict__ part_p,
-                       int* __restrict__ part_c, int* __restrict__ part_n, int* __restrict__ ticket)
+                       int* __restrict__ part_c, int* __restrict__ part_n, int* __restrict__ ticket,
+                       float* __restrict__ prob, int* __restrict__ counts, int* __restrict__ tokens,
+                       float* __restrict__ loss)
 {
-    __shared__ float s_p[kBalThreads / 32][EPL * 32];
-    __shared__ int s_c[EPL * 32];
-    __shared__ int s_n;
+    constexpr int R = 32 / LPR;                       // rows of a warp
+    __shared__ float s_p[kBalWarps][LPR * kBalPer];
+    __shared__ int s_c[256];
+    __shared__ int s_n, s_g;
+    __shared__ float s_w[kBalWarps];
     pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane % LPR;
     if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;
-    const int t0 = blockIdx.x * kBalRun, t1 = min(n_tok, t0 + kBalRun);
+    const int t0 = (int)min((long long)blockIdx.x * run, (long long)n_tok);
+    const int t1 = (int)min((long long)t0 + run, (long long)n_tok);
+    const bool alone = gridDim.x == 1 && !cu;         // one run, one group: finished here
     const int g_end = cu ? n_seq : 1;
-    for (int g = cu ? bal_group(cu, n_seq, t0) : 0; g < g_end; ++g) {
+    for (int g = cu ? bal_group_block(cu, n_seq, t0, &s_g) : 0; g < g_end; ++g) {
         const int a = cu ? max(t0, bal_bound(cu, g, n_tok)) : t0;
         const int b = cu ? min(t1, bal_bound(cu, g + 1, n_tok)) : t1;
-        if (a >= t1) break;
-        if (a >= b) continue;
-        for (int e = threadIdx.x; e < E; e += kBalThreads) s_c[e] = 0;
+        if (a >= t1 && !alone) break;
+        if (a >= b && !alone) continue;
+        if (threadIdx.x < E) s_c[threadIdx.x] = 0;
         if (threadIdx.x == 0) s_n = 0;
         __syncthreads();
-        float acc[EPL];
+        float acc[kBalPer], v[kBalPer];
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) acc[j] = 0.f;
+        for (int j = 0; j < kBalPer; ++j) acc[j] = 0.f;
         int n = 0;
-        for (int t = a + warp; t < b; t += kBalThreads / 32) {
-            if (valid && !valid[t]) continue;
-            ++n;
-            float v[EPL];
+        // rows of this lane, kBalWarps * R apart; the next row is loaded before this one is used.  A row
+        // that does not count is loaded like the others (no load waits for another) and dropped.
+        int t = a + warp * R + lane / LPR;
+        bool on = t < b && (!valid || valid[t]);
+        bal_load<T, LPR>(v, logits + (long long)t * ldl, r, E, t < b);
+        // counts: one thread per (token, slot)
+        const int* ids = topk + (long long)a * K;
+        for (int i = threadIdx.x; i < (b - a) * K; i += kBalThreads) {
+            const int id = __ldg(ids + i);
+            const bool counts_too = !valid || valid[a + i / K];
+            if (id >= 0 && id < E && counts_too) atomicAdd(&s_c[id], 1);
+        }
+        for (int base = a + warp * R; base < b; base += kBalWarps * R) {
+            float w[kBalPer];
+            const bool cur = on;
+            t += kBalWarps * R;
+            on = t < b && (!valid || valid[t]);
+            bal_load<T, LPR>(w, logits + (long long)t * ldl, r, E, t < b);
+            bal_softmax<LPR>(v);
+            if (cur) {
+                ++n;
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) {
-                const int e = lane + 32 * j;
-                v[j] = e < E ? to_float(logits[(long long)t * ldl + e]) : -INFINITY;
+                for (int j = 0; j < kBalPer; ++j) acc[j] += v[j];
             }
-            bal_softmax<EPL>(v);
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) acc[j] += v[j];
-            if (lane < K) {
-                const int id = topk[(long long)t * K + lane];
-                if (id >= 0 && id < E) atomicAdd(&s_c[id], 1);
-            }
+            for (int j = 0; j < kBalPer; ++j) v[j] = w[j];
         }
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) s_p[warp][lane + 32 * j] = acc[j];
-        if (lane == 0 && n) atomicAdd(&s_n, n);
-        __syncthreads();
-        const long long slot = (long long)blockIdx.x + g;
-        for (int e = threadIdx.x; e < E; e += kBalThreads) {
-            float s = 0.f;
+        for (int j = 0; j < kBalPer; ++j) {
 #pragma unroll
-            for (int w = 0; w < kBalThreads / 32; ++w) s += s_p[w][e];
-            part_p[slot * E + e] = s;
+            for (int o = LPR; o < 32; o <<= 1) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
+            if (lane < LPR) s_p[warp][r + LPR * j] = acc[j];
+        }
+        if (r == 0 && n) atomicAdd(&s_n, n);
+        __syncthreads();
+        const int e = threadIdx.x;
+        float sum = 0.f;
+        if (e < E)
+#pragma unroll
+            for (int w = 0; w < kBalWarps; ++w) sum += s_p[w][e];
+        if (alone) {
+            const float l = bal_finish(0, e, E, K, sum, e < E ? s_c[e] : 0, s_n, prob, counts, tokens, s_w);
+            if (threadIdx.x == 0) *loss = l;
+            break;
+        }
+        const long long slot = (long long)blockIdx.x + g;
+        if (e < E) {
+            part_p[slot * E + e] = sum;
             part_c[slot * E + e] = s_c[e];
         }
-        if (threadIdx.x == 0) part_n[slot] = s_n;
+        if (e == 0) part_n[slot] = s_n;
         __syncthreads();
     }
     pdl_launch_dependents();
 }
 
-__global__ void __launch_bounds__(256)
+// EP: the power of two that holds min(E, 32); 1024 / EP threads share an expert's slots.  (One CTA per
+// group would read all slots through one SM: 600 KB for 16384 tokens of 256 experts.)
+__global__ void __launch_bounds__(kBalReduceThreads)
 balance_reduce_kernel(const float* __restrict__ part_p, const int* __restrict__ part_c,
-                      const int* __restrict__ part_n, int n_tok, int E, int K,
-                      const int* __restrict__ cu, float* __restrict__ loss_g,
+                      const int* __restrict__ part_n, int n_tok, int E, int EP, int K, int run,
+                      const int* __restrict__ cu, float* __restrict__ loss_part,
                       int* __restrict__ ticket, float* __restrict__ prob, int* __restrict__ counts,
                       int* __restrict__ tokens, float* __restrict__ loss)
 {
-    __shared__ float s_l[8];
+    __shared__ float s_p[kBalReduceThreads];
+    __shared__ int s_c[kBalReduceThreads];
+    __shared__ float s_w[kBalReduceThreads / 32];
     __shared__ int s_n, s_last;
     pdl_wait();
-    const int g = blockIdx.x;
+    const int g = blockIdx.x, tid = threadIdx.x, e0 = blockIdx.y * 32;
     const int a = cu ? bal_bound(cu, g, n_tok) : 0, b = cu ? bal_bound(cu, g + 1, n_tok) : n_tok;
-    const int c0 = a / kBalRun, c1 = b > a ? (b - 1) / kBalRun + 1 : c0;
-    if (threadIdx.x == 0) s_n = 0;
+    const int c0 = a / run, c1 = b > a ? (b - 1) / run + 1 : c0;
+    if (tid == 0) s_n = 0;
     __syncthreads();
     int n = 0;
-    for (int c = c0 + threadIdx.x; c < c1; c += blockDim.x) n += part_n[c + g];
+    for (int c = c0 + tid; c < c1; c += kBalReduceThreads) n += part_n[c + g];
     if (n) atomicAdd(&s_n, n);
-    __syncthreads();
-    n = s_n;
-    float l = 0.f;
-    const int e = threadIdx.x;
-    if (e < E) {
-        float s = 0.f;
-        int cnt = 0;
-        for (int c = c0; c < c1; ++c) {
-            s += part_p[(long long)(c + g) * E + e];
-            cnt += part_c[(long long)(c + g) * E + e];
+    const int e = e0 + (tid & (EP - 1)), subs = kBalReduceThreads / EP, sub = tid / EP;
+    float sum = 0.f;
+    int cnt = 0;
+    if (e < E)
+#pragma unroll 8
+        for (int c = c0 + sub; c < c1; c += subs) {
+            sum += __ldg(part_p + (long long)(c + g) * E + e);
+            cnt += __ldg(part_c + (long long)(c + g) * E + e);
         }
-        const float p = n ? s / (float)n : 0.f;
-        prob[(long long)g * E + e] = p;
-        counts[(long long)g * E + e] = cnt;
-        if (n) l = p * ((float)((double)cnt * E / ((double)K * n)));
-    }
-    l = warp_sum(l);
-    if ((threadIdx.x & 31) == 0) s_l[threadIdx.x >> 5] = l;
+    s_p[tid] = sum;
+    s_c[tid] = cnt;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        float s = 0.f;
-        for (int w = 0; w < 8; ++w) s += s_l[w];
-        loss_g[g] = s;
-        tokens[g] = n;
+    // halve the threads that share an expert until one is left: the same order whatever the timing
+    for (int o = kBalReduceThreads / 2; o >= EP; o >>= 1) {
+        if (tid < o) { s_p[tid] += s_p[tid + o]; s_c[tid] += s_c[tid + o]; }
+        __syncthreads();
+    }
+    const float l = bal_finish(g, tid < EP ? e : E, E, K, s_p[tid], s_c[tid], s_n, prob, counts, tokens, s_w);
+    if (tid == 0) {
+        loss_part[(long long)g * gridDim.y + blockIdx.y] = l;
         __threadfence();
-        s_last = atomicAdd(ticket, 1) == (int)gridDim.x - 1;
+        s_last = atomicAdd(ticket, 1) == (int)(gridDim.x * gridDim.y) - 1;
     }
     __syncthreads();
-    if (s_last && threadIdx.x < 32) {
+    if (s_last) {
         __threadfence();
-        float s = 0.f;
-        int act = 0;
-        for (int i = threadIdx.x; i < (int)gridDim.x; i += 32) {
-            s += __ldcg(loss_g + i);
-            act += __ldcg(tokens + i) > 0;
-        }
-        s = warp_sum(s);
-        act = __reduce_add_sync(0xffffffffu, act);
-        if (threadIdx.x == 0) *loss = act ? s / (float)act : 0.f;
+        float s = 0.f, act = 0.f;
+        for (long long i = tid; i < (long long)gridDim.x * gridDim.y; i += kBalReduceThreads) s += __ldcg(loss_part + i);
+        for (int i = tid; i < (int)gridDim.x; i += kBalReduceThreads) act += __ldcg(tokens + i) > 0 ? 1.f : 0.f;
+        s = bal_block_sum(s, s_w);
+        act = bal_block_sum(act, s_w);
+        if (tid == 0) *loss = act > 0.f ? s / act : 0.f;
     }
     pdl_launch_dependents();
 }
 
-template <typename T, int EPL>
+// One warp's slot gradients: (row of the warp, slot) pairs, 32 at a time, added to the rows in shared
+// memory in slot order.  An expert chosen twice by a row gets its terms one after the other.
+template <int LPR>
+__device__ __forceinline__ void bal_add_slots(float* rows, int n_rows, int E, int K, const int* __restrict__ ids,
+                                              const float* __restrict__ d_r, const float* __restrict__ d_l, int lane)
+{
+    for (int i0 = 0; i0 < n_rows * K; i0 += 32) {
+        const int i = i0 + lane;
+        int id = -1, row = 0;
+        float gr = 0.f, gl = 0.f;
+        if (i < n_rows * K) {
+            id = __ldg(ids + i);
+            gr = __ldg(d_r + i);
+            gl = __ldg(d_l + i);
+            row = i / K;
+        }
+        const bool on = id >= 0 && id < E;
+        const int key = on ? row * 256 + id : -1 - lane;
+        const unsigned same = __match_any_sync(0xffffffffu, key);
+        const bool twice = __any_sync(0xffffffffu, (same & (same - 1)) != 0);
+        float* p = rows + row * 2 * E + id;
+        if (!twice) {
+            if (on) { p[0] += gr; p[E] += gl; }
+        } else {
+            for (int k = 0; k < 32; ++k) {
+                if (lane == k && on) { p[0] += gr; p[E] += gl; }
+                __syncwarp();
+            }
+        }
+        __syncwarp();
+    }
+}
+
+template <typename T, int LPR>
 __global__ void __launch_bounds__(kBalThreads)
-balance_grad_kernel(const T* __restrict__ logits, long long ldl, int n_tok, int E,
+balance_grad_kernel(const T* __restrict__ logits, long long ldl, int n_tok, int E, int run,
                     const int* __restrict__ topk, int K, const uint8_t* __restrict__ valid,
                     const int* __restrict__ cu, int n_seq, const int* __restrict__ counts,
                     const int* __restrict__ tokens, float scale, const float* __restrict__ d_r,
                     const float* __restrict__ d_l, float* __restrict__ out)
 {
-    __shared__ int s_act;
+    constexpr int R = 32 / LPR;
+    __shared__ float s_rows[kBalWarps][R * 2 * LPR * kBalPer];
+    __shared__ int s_act, s_g;
     pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane % LPR;
+    const int G = cu ? n_seq : 1;
     if (threadIdx.x == 0) s_act = 0;
     __syncthreads();
-    const int G = cu ? n_seq : 1;
     int act = 0;
     for (int i = threadIdx.x; i < G; i += kBalThreads) act += tokens[i] > 0;
     if (act) atomicAdd(&s_act, act);
+    const long long t0 = (long long)blockIdx.x * run, t1 = min(t0 + run, (long long)n_tok);
+    int g = cu ? bal_group_block(cu, n_seq, (int)t0, &s_g) : 0;   // moves on with the lane's rows
+    float v[kBalPer], f[kBalPer];
+    float coef = 0.f;
+    int g_of_f = -1;
+    const int width = d_r ? 2 * E : E;
+    float* rows = s_rows[warp];
     __syncthreads();
     act = s_act;
-    const long long t = (long long)blockIdx.x * (kBalThreads / 32) + warp;
-    if (t < n_tok) {
-        float d[EPL], dm[EPL];
+    long long t = t0 + warp * R + lane / LPR;
+    bool here = t < t1;
+    bal_load<T, LPR>(v, logits + t * ldl, r, E, here);
+    for (long long base = t0 + warp * R; base < t1; base += kBalWarps * R) {
+        // the row's group, and f of that group where it is another than the last row's
+        bool in = here && (!valid || valid[t]);
+        if (cu && in) {
+            while (g < G && __ldg(cu + g + 1) <= t) ++g;
+            in = g < G && bal_bound(cu, g, n_tok) <= t;
+        }
+        if (in && g != g_of_f) {
+            const int n = tokens[g];
+            const float inv_kn = n > 0 ? 1.0f / ((float)K * (float)n) : 0.f;
+            coef = n > 0 ? scale / ((float)act * (float)n) : 0.f;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) d[j] = dm[j] = 0.f;
-        const int g = cu ? bal_group(cu, n_seq, (int)t) : 0;
-        const bool in = g < G && (!cu || bal_bound(cu, g, n_tok) <= t) && (!valid || valid[t]);
-        const int n = in ? tokens[g] : 0;
-        if (n > 0) {
-#pragma unroll
-            for (int j = 0; j < EPL; ++j) {
-                const int e = lane + 32 * j;
-                d[j] = e < E ? to_float(logits[t * ldl + e]) : -INFINITY;
-            }
-            bal_softmax<EPL>(d);
-            const float inv_kn = 1.0f / ((float)K * (float)n);
-            float f[EPL], dot = 0.f;
-#pragma unroll
-            for (int j = 0; j < EPL; ++j) {
-                const int e = lane + 32 * j;
+            for (int j = 0; j < kBalPer; ++j) {
+                const int e = r + LPR * j;
                 f[j] = e < E ? (float)((long long)counts[(long long)g * E + e] * E - (long long)K * n) * inv_kn : 0.f;
-                dot += f[j] * d[j];
             }
-            dot = warp_sum(dot);
-            const float coef = scale / ((float)act * (float)n);
-#pragma unroll
-            for (int j = 0; j < EPL; ++j) d[j] = coef * d[j] * (f[j] - dot);
+            g_of_f = g;
         }
-        const int ldo = d_r ? 2 * E : E;
-        if (d_r) {
-            for (int k = 0; k < K; ++k) {
-                const long long o = t * K + k;
-                const int id = topk[o];
-                const float gr = d_r[o], gl = d_l[o];
+        float w[kBalPer];
+        const bool cur = in && coef != 0.f;
+        t += kBalWarps * R;
+        here = t < t1;
+        bal_load<T, LPR>(w, logits + t * ldl, r, E, here);
+        bal_softmax<LPR>(v);
+        float dot = 0.f;
 #pragma unroll
-                for (int j = 0; j < EPL; ++j)
-                    if (id == lane + 32 * j) { d[j] += gr; dm[j] += gl; }
-            }
-        }
+        for (int j = 0; j < kBalPer; ++j) dot += cur ? f[j] * v[j] : 0.f;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            const int e = lane + 32 * j;
+        for (int o = LPR / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        float* row = rows + (lane / LPR) * width;
+#pragma unroll
+        for (int j = 0; j < kBalPer; ++j) {
+            const int e = r + LPR * j;
             if (e < E) {
-                out[t * ldo + e] = d[j];
-                if (d_r) out[t * ldo + E + e] = dm[j];
+                row[e] = cur ? coef * v[j] * (f[j] - dot) : 0.f;
+                if (d_r) row[E + e] = 0.f;
             }
         }
+        __syncwarp();
+        const int n_rows = (int)min((long long)R, t1 - base);
+        if (d_r) bal_add_slots<LPR>(rows, n_rows, E, K, topk + base * K, d_r + base * K, d_l + base * K, lane);
+        // the rows are contiguous in memory
+        float* o = out + base * width;
+        const int total = n_rows * width;
+        if ((reinterpret_cast<uintptr_t>(o) & 15) == 0 && (total & 3) == 0) {
+            for (int i = lane; i < total / 4; i += 32)
+                reinterpret_cast<float4*>(o)[i] = reinterpret_cast<const float4*>(rows)[i];
+        } else {
+            for (int i = lane; i < total; i += 32) o[i] = rows[i];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < kBalPer; ++j) v[j] = w[j];
     }
     pdl_launch_dependents();
 }

@@ -76,7 +76,7 @@ struct BalArgs {
 
 static beam_status_t check_balance(const BalArgs& a)
 {
-    if (a.T < 0) FAIL_ARG("T=%d is negative", a.T);
+    if (a.T < 0 || a.T > (1 << 30)) FAIL_ARG("T=%d outside [0, 2^30]", a.T);
     if (a.E < 1 || a.E > kMaxExperts) FAIL_ARG("E=%d must be in [1, %d]", a.E, kMaxExperts);
     if (a.K < 1 || a.K > kMaxSlots) FAIL_ARG("K=%d must be in [1, %d]", a.K, kMaxSlots);
     if (a.cu ? (a.n_seq < 1 || a.n_seq > 65536) : a.n_seq != 0)
@@ -87,7 +87,20 @@ static beam_status_t check_balance(const BalArgs& a)
     return BEAM_OK;
 }
 
-static long long bal_runs(int T) { return std::max(1LL, ceil_div(T, kBalRun)); }
+// Lanes that share a row of E logits, 8 values each.
+static int bal_lanes(int E)
+{
+    int l = 1;
+    while (l * kBalPer < E) l *= 2;
+    return l;
+}
+// Tokens of a run: whole passes of a CTA's rows, as few as keep the runs at kBalRuns or below.
+static int bal_run(int T, int E)
+{
+    const long long pass = (long long)kBalWarps * (32 / bal_lanes(E));
+    return (int)std::max(pass, ceil_div(ceil_div(T, kBalRuns), pass) * pass);
+}
+static long long bal_runs(int T, int E) { return std::max(1LL, ceil_div(T, bal_run(T, E))); }
 
 // Workspace: part_p, part_c [slots][E], part_n [slots], the groups' losses, the ticket.
 struct BalWork { long long slots, p, c, n, lg, ticket, bytes; };
@@ -95,54 +108,58 @@ static BalWork bal_work(int T, int E, int n_seq)
 {
     BalWork w;
     const int G = std::max(1, n_seq);
-    w.slots = bal_runs(T) + G;
+    w.slots = bal_runs(T, E) + G;
     w.p = 0;
     w.c = align256(w.p + w.slots * E * 4);
     w.n = align256(w.c + w.slots * E * 4);
     w.lg = align256(w.n + w.slots * 4);
-    w.ticket = align256(w.lg + G * 4LL);
+    w.ticket = align256(w.lg + G * ceil_div(E, 32) * 4);
     w.bytes = w.ticket + 256;
     return w;
 }
 
-template <typename T, int EPL>
-static cudaError_t launch_balance(const BalArgs& a, char* ws, const BalWork& w, cudaStream_t st)
-{
-    return launch_free(balance_partial_kernel<T, EPL>, dim3((unsigned)bal_runs(a.T)), dim3(kBalThreads), 0, st,
-                       (const T*)a.logits, a.ldl, a.T, a.E, a.topk, a.K, a.valid, a.cu, a.n_seq,
-                       (float*)(ws + w.p), (int*)(ws + w.c), (int*)(ws + w.n), (int*)(ws + w.ticket));
-}
-
-template <typename T, int EPL>
-static cudaError_t launch_balance_grad(const BalArgs& a, const int32_t* counts, const int32_t* tokens, float scale,
-                                       const float* dr, const float* dl, float* out, cudaStream_t st)
-{
-    return launch_free(balance_grad_kernel<T, EPL>, dim3((unsigned)ceil_div(a.T, kBalThreads / 32)),
-                       dim3(kBalThreads), 0, st, (const T*)a.logits, a.ldl, a.T, a.E, a.topk, a.K, a.valid,
-                       a.cu, a.n_seq, counts, tokens, scale, dr, dl, out);
-}
-
-// Calls FN<T, EPL>(...) for the row width: EPL = logits per lane.
+// Calls FN<T, LPR>(...) for the row width.
 #define BAL_DISPATCH(FN, ...)                                                                   \
     with_type(a.dtype, [&](auto z) -> cudaError_t {                                             \
         using T_ = decltype(z);                                                                 \
-        switch ((a.E + 31) / 32) {                                                              \
+        switch (bal_lanes(a.E)) {                                                               \
             case 1: return FN<T_, 1>(__VA_ARGS__);                                              \
             case 2: return FN<T_, 2>(__VA_ARGS__);                                              \
-            case 3: return FN<T_, 3>(__VA_ARGS__);                                              \
             case 4: return FN<T_, 4>(__VA_ARGS__);                                              \
-            case 5: return FN<T_, 5>(__VA_ARGS__);                                              \
-            case 6: return FN<T_, 6>(__VA_ARGS__);                                              \
-            case 7: return FN<T_, 7>(__VA_ARGS__);                                              \
-            default: return FN<T_, 8>(__VA_ARGS__);                                             \
+            case 8: return FN<T_, 8>(__VA_ARGS__);                                              \
+            case 16: return FN<T_, 16>(__VA_ARGS__);                                            \
+            default: return FN<T_, 32>(__VA_ARGS__);                                            \
         }                                                                                       \
     })
+
+struct BalOut { float *loss, *prob; int32_t *counts, *tokens; };
+
+template <typename T, int LPR>
+static cudaError_t launch_balance(const BalArgs& a, char* ws, const BalWork& w, const BalOut& o, cudaStream_t st)
+{
+    return launch_free(balance_partial_kernel<T, LPR>, dim3((unsigned)bal_runs(a.T, a.E)), dim3(kBalThreads), 0, st,
+                       (const T*)a.logits, a.ldl, a.T, a.E, bal_run(a.T, a.E), a.topk, a.K, a.valid, a.cu, a.n_seq,
+                       (float*)(ws + w.p), (int*)(ws + w.c), (int*)(ws + w.n), (int*)(ws + w.ticket), o.prob,
+                       o.counts, o.tokens, o.loss);
+}
+
+template <typename T, int LPR>
+static cudaError_t launch_balance_grad(const BalArgs& a, const int32_t* counts, const int32_t* tokens, float scale,
+                                       const float* dr, const float* dl, float* out, cudaStream_t st)
+{
+    // one or two passes per CTA for ordinary batches, up to eight CTAs per SM
+    const long long pass = (long long)kBalWarps * (32 / LPR);
+    const int run = (int)std::max(pass, ceil_div(ceil_div(a.T, 148 * 8), pass) * pass);
+    return launch_free(balance_grad_kernel<T, LPR>, dim3((unsigned)ceil_div(a.T, run)), dim3(kBalThreads), 0, st,
+                       (const T*)a.logits, a.ldl, a.T, a.E, run, a.topk, a.K, a.valid, a.cu, a.n_seq, counts, tokens,
+                       scale, dr, dl, out);
+}
 
 extern "C" {
 
 int64_t beam_balance_workspace(int32_t T, int32_t E, int32_t n_seq)
 {
-    if (T < 0 || E < 1 || E > kMaxExperts || n_seq < 0 || n_seq > 65536) return -1;
+    if (T < 0 || T > (1 << 30) || E < 1 || E > kMaxExperts || n_seq < 0 || n_seq > 65536) return -1;
     return bal_work(T, E, n_seq).bytes;
 }
 
@@ -163,10 +180,16 @@ beam_status_t beam_balance_forward(const void* logits, int32_t dtype, int32_t T,
         FAIL_ARG("the workspace must be 16-byte aligned and hold %lld bytes", w.bytes);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
-    BEAM_HOST_CUDA(BAL_DISPATCH(launch_balance, a, ws, w, st));
-    BEAM_HOST_CUDA(launch_free(balance_reduce_kernel, dim3((unsigned)std::max(1, n_seq)), dim3(256), 0, st,
-                               (const float*)(ws + w.p), (const int*)(ws + w.c), (const int*)(ws + w.n), T, E, K,
-                               cu_seqlens, (float*)(ws + w.lg), (int*)(ws + w.ticket), prob, counts, tokens, loss));
+    const BalOut o{loss, prob, counts, tokens};
+    BEAM_HOST_CUDA(BAL_DISPATCH(launch_balance, a, ws, w, o, st));
+    if (bal_runs(T, E) == 1 && !cu_seqlens) return BEAM_OK;   // finished by its only CTA
+    int ep = 1;
+    while (ep < std::min(E, 32)) ep *= 2;
+    const dim3 grid((unsigned)std::max(1, n_seq), (unsigned)ceil_div(E, 32));
+    BEAM_HOST_CUDA(launch_free(balance_reduce_kernel, grid, dim3(kBalReduceThreads), 0,
+                               st, (const float*)(ws + w.p), (const int*)(ws + w.c), (const int*)(ws + w.n), T, E, ep,
+                               K, bal_run(T, E), cu_seqlens, (float*)(ws + w.lg), (int*)(ws + w.ticket), prob, counts,
+                               tokens, loss));
     return BEAM_OK;
 }
 
