@@ -204,16 +204,22 @@ __device__ __forceinline__ uint32_t pack_hi(uint32_t lo, uint32_t hi) { return _
 
 // bf16 limbs of the eight values, most significant first.
 __device__ __forceinline__ void raw_limbs(const Raw<SRC_BF16>& r, uint4* o) { o[0] = r.a; }
+// q 2^k in pairs of bf16.  With u = q + 128 = 128 h + l, the byte l under 0x43 is the bf16 number 128 + l, and
+// the byte 128 (1 - h) under 0x43 is 128 or 256: their difference is q, exactly (8 significant bits), and so
+// is its product with 2^k.  (Going by float32 takes half as many instructions again.)
+__device__ __forceinline__ uint32_t ckpt_pair(uint32_t w, uint32_t sel, __nv_bfloat162 step)
+{
+    const uint32_t a = __byte_perm(w & 0x7f7f7f7fu, 0x43u, sel), c = __byte_perm(w & 0x80808080u, 0x43u, sel);
+    const __nv_bfloat162 q = __hsub2(reinterpret_cast<const __nv_bfloat162&>(a), reinterpret_cast<const __nv_bfloat162&>(c));
+    const __nv_bfloat162 v = __hmul2(q, step);
+    return reinterpret_cast<const uint32_t&>(v);
+}
 __device__ __forceinline__ void raw_limbs(const Raw<SRC_CKPT>& r, uint4* o)
 {
-    float f[8];
-    ckpt_unpack4(r.w.x, f);
-    ckpt_unpack4(r.w.y, f + 4);
-    const float step = ckpt_step(r.byte);
-    uint32_t u[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(f[j] * step);   // exact in bf16
-    o[0] = make_uint4(pack_hi(u[0], u[1]), pack_hi(u[2], u[3]), pack_hi(u[4], u[5]), pack_hi(u[6], u[7]));
+    const uint32_t k = (uint32_t)r.byte << 7, k2 = k | k << 16;
+    const __nv_bfloat162 step = reinterpret_cast<const __nv_bfloat162&>(k2);
+    o[0] = make_uint4(ckpt_pair(r.w.x, 0x4140, step), ckpt_pair(r.w.x, 0x4342, step), ckpt_pair(r.w.y, 0x4140, step),
+                      ckpt_pair(r.w.y, 0x4342, step));
 }
 __device__ __forceinline__ void raw_limbs(const Raw<SRC_F32>& r, uint4* o)
 {
@@ -304,13 +310,16 @@ template <int SRC, bool MN, int ROWS> struct Cursor {
 };
 static_assert(kCkptBlock == 32, "the scale of a value is found by shifts of 5");
 
+// at: an address of the shared window.
 template <int SRC, int LIMB>
-__device__ __forceinline__ void piece_store(const Raw<SRC>& r, uint8_t* at)
+__device__ __forceinline__ void piece_store(const Raw<SRC>& r, uint32_t at)
 {
     uint4 l[limbs(SRC)];
     raw_limbs(r, l);
 #pragma unroll
-    for (int i = 0; i < limbs(SRC); ++i) *reinterpret_cast<uint4*>(at + i * LIMB) = l[i];
+    for (int i = 0; i < limbs(SRC); ++i)
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + i * LIMB), "r"(l[i].x), "r"(l[i].y),
+                     "r"(l[i].z), "r"(l[i].w) : "memory");
 }
 
 // Shared-memory descriptor of an MN-major tile: blocks of 64 values (128 bytes) of m or n, 64 rows of k
@@ -380,8 +389,9 @@ lin_gemm_kernel(const __grid_constant__ Params p)
         const uint32_t oa = CA::offset(tid), ob = CB::offset(tid) + ring + bpart;
         CA ca;
         CB cb;
-        // Two sets of registers: a step is loaded while the one before the next is converted.
-        struct Set { Raw<SA> a[RES ? 1 : PA]; Raw<SB> b[PB]; } set0, set1;
+        // The registers of one step: each piece is loaded again as soon as it is converted.  (Two sets, a step
+        // further ahead, measured slower: 40 against 38 us for 8192 x 1536 x 424.)
+        struct Set { Raw<SA> a[RES ? 1 : PA]; Raw<SB> b[PB]; } set;
         Unit t = {};
         int u = pair, left = 0;
         auto start_tile = [&]() {
@@ -419,7 +429,7 @@ lin_gemm_kernel(const __grid_constant__ Params p)
         // piece by piece.  ALL: that one lies inside k: plain loads.
         auto body = [&](Set& r, auto all) {
             constexpr bool ALL = decltype(all)::value;
-            uint8_t* sm = gbase + s * kStage;
+            const uint32_t sm = base + s * kStage;
             if (!RES)
 #pragma unroll
                 for (int i = 0; i < PA; ++i) {
@@ -449,7 +459,7 @@ lin_gemm_kernel(const __grid_constant__ Params p)
                     for (int i = 0; i < PA; ++i) ca.template load<VEC>(v[i], i, p.K);
 #pragma unroll
                     for (int i = 0; i < PA; ++i)
-                        piece_store<SA, kLimbA>(v[i], gbase + k * (LA * kLimbA) + oa + i * (CA::kRows * 128));
+                        piece_store<SA, kLimbA>(v[i], base + k * (LA * kLimbA) + oa + i * (CA::kRows * 128));
                     ca.advance(p.a);
                 }
                 rest = (c.nt1 - c.nt) * p.k_steps;
@@ -466,18 +476,11 @@ lin_gemm_kernel(const __grid_constant__ Params p)
             if (++s == ST) { s = 0; ph ^= 1u; }
             return true;
         };
-        fill(set0);
-        next();
-        fill(set1);
-        bool v1 = more;
+        fill(set);
         next();
         while (true) {
             const bool v0 = more;
-            if (!process(set0)) break;
-            next();
-            if (!v1) break;
-            v1 = more;
-            if (!process(set1)) break;
+            if (!process(set)) break;
             next();
             if (!v0) break;
         }

@@ -17,6 +17,13 @@ from ._lib import BEAM_DTYPE_BF16, BEAM_DTYPE_F16, BEAM_DTYPE_F32, check
 _DTYPES = {torch.float32: BEAM_DTYPE_F32, torch.bfloat16: BEAM_DTYPE_BF16}
 _CKPT_DTYPES = {**_DTYPES, torch.float16: BEAM_DTYPE_F16}
 CKPT_BLOCK = 32   # columns that share a scale
+# (torch.empty is called with the sizes as separate arguments throughout: a tuple of them costs a
+# microsecond more, and a small call launches in five.)
+
+
+@functools.lru_cache(maxsize=1024)
+def _balance_workspace(T: int, E: int, n_seq: int) -> int:
+    return _lib.load().beam_balance_workspace(T, E, n_seq)
 
 
 def _on_stream(fn):
@@ -94,12 +101,12 @@ def balance_loss(logits: torch.Tensor, topk_id: torch.Tensor, valid: torch.Tenso
     K, ids, v, cu, n = _groups(T, dev, topk_id, valid, cu_seqlens)
     lib = _lib.load()
     G = max(1, n)
-    size = lib.beam_balance_workspace(T, E, n)
+    size = _balance_workspace(T, E, n)
     loss = torch.empty((), dtype=torch.float32, device=dev)
-    prob = torch.empty((G, E), dtype=torch.float32, device=dev)
-    counts = torch.empty((G, E), dtype=torch.int32, device=dev)
-    tokens = torch.empty((G,), dtype=torch.int32, device=dev)
-    ws = torch.empty((max(size, 0),), dtype=torch.uint8, device=dev)
+    prob = torch.empty(G, E, dtype=torch.float32, device=dev)
+    counts = torch.empty(G, E, dtype=torch.int32, device=dev)
+    tokens = torch.empty(G, dtype=torch.int32, device=dev)
+    ws = torch.empty(max(size, 0), dtype=torch.uint8, device=dev)
     check(lib.beam_balance_forward(logits.data_ptr(), dt, T, E, ld, ids, K, v, cu, n,
                                    loss.data_ptr(), prob.data_ptr(), counts.data_ptr(),
                                    tokens.data_ptr(), ws.data_ptr(), size, _stream(dev)))
@@ -129,7 +136,7 @@ def balance_loss_backward(logits: torch.Tensor, topk_id: torch.Tensor, balance: 
     if d_gate_logit is not None:
         gr = _array("d_gate_logit", d_gate_logit, torch.float32, (T, K), dev)
         gl = _array("d_mask_logit", d_mask_logit, torch.float32, (T, K), dev)
-    out = torch.empty((T, E if gr is None else 2 * E), dtype=torch.float32, device=dev)
+    out = torch.empty(T, E if gr is None else 2 * E, dtype=torch.float32, device=dev)
     check(_lib.load().beam_balance_backward(logits.data_ptr(), dt, T, E, ld, ids, K, v, cu,
                                             n, counts, tokens, scale, gr, gl, out.data_ptr(), _stream(dev)))
     return out
@@ -143,8 +150,8 @@ def checkpoint_save(x: torch.Tensor) -> dict:
     Rows may be taken out of q and scale by indexing both alike.  See beam_checkpoint_save."""
     dt, n, d, ld = _matrix("x", x, _CKPT_DTYPES)
     dev, nb = x.device, -(-d // CKPT_BLOCK)
-    q = torch.empty((n, nb * CKPT_BLOCK), dtype=torch.int8, device=dev)
-    scale = torch.empty((n, nb), dtype=torch.uint8, device=dev)
+    q = torch.empty(n, nb * CKPT_BLOCK, dtype=torch.int8, device=dev)
+    scale = torch.empty(n, nb, dtype=torch.uint8, device=dev)
     check(_lib.load().beam_checkpoint_save(x.data_ptr(), dt, n, d, ld, q.data_ptr(),
                                            scale.data_ptr(), _stream(dev)))
     return dict(q=q, scale=scale, d=d)
@@ -168,7 +175,7 @@ def checkpoint_load(ckpt: dict, dtype: torch.dtype = torch.float32) -> torch.Ten
         raise TypeError(f"unsupported dtype {dtype}")
     q, scale, n, d = _checkpoint(ckpt)
     dev = ckpt["q"].device
-    y = torch.empty((n, d), dtype=dtype, device=dev)
+    y = torch.empty(n, d, dtype=dtype, device=dev)
     check(_lib.load().beam_checkpoint_load(q, scale, n, d, y.data_ptr(), dt, _stream(dev)))
     return y
 
@@ -191,7 +198,7 @@ def checkpoint_route_grad(ckpt: dict, gate: torch.Tensor, mask_logit: torch.Tens
     if rows != T or cols != d or n != T * K:
         raise ValueError(f"dy must be [T][d] and the checkpoint hold T*K rows: got dy {tuple(dy.shape)}, "
                          f"{n} rows of {d} values, gate {(T, K)}")
-    out = [torch.empty((T, K), dtype=torch.float32, device=dev) for _ in range(3)]
+    out = [torch.empty(T, K, dtype=torch.float32, device=dev) for _ in range(3)]
     check(_lib.load().beam_checkpoint_route_grad(q, scale, T, K, d, g, l, dy.data_ptr(), dt, ld,
                                                  segment_len, reg_scale, out[0].data_ptr(),
                                                  out[1].data_ptr(), out[2].data_ptr(), _stream(dev)))
@@ -210,10 +217,11 @@ def router_weight_grad(ckpt: dict, dlogits: torch.Tensor, parts: int = 1) -> tor
         raise ValueError(f"dlogits has {T} rows, the checkpoint {n}")
     if parts < 1 or C % parts:
         raise ValueError(f"parts={parts} must divide the {C} columns of dlogits")
-    dw = torch.empty((d, C) if parts == 1 else (parts, d, C // parts), dtype=torch.float32, device=dev)
+    f32 = dict(dtype=torch.float32, device=dev)
+    dw = torch.empty(d, C, **f32) if parts == 1 else torch.empty(parts, d, C // parts, **f32)
     lib = _lib.load()
     size = lib.beam_router_weight_grad_workspace(T, d, C)
-    ws = torch.empty((size,), dtype=torch.uint8, device=dev) if size > 0 else None
+    ws = torch.empty(size, dtype=torch.uint8, device=dev) if size > 0 else None
     check(lib.beam_router_weight_grad(q, scale, T, d, dlogits.data_ptr(), dt, ld, C, parts, dw.data_ptr(),
                                       None if ws is None else ws.data_ptr(), size, _stream(dev)))
     return dw
@@ -228,7 +236,7 @@ def router_input_grad(dlogits: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
     wt, d, cols, lw = _matrix("w", w, _DTYPES, dev)
     if cols != C:
         raise ValueError(f"w must have dlogits' {C} columns")
-    dx = torch.empty((T, d), dtype=torch.float32, device=dev)
+    dx = torch.empty(T, d, dtype=torch.float32, device=dev)
     check(_lib.load().beam_router_input_grad(dlogits.data_ptr(), dt, ld, T, C, w.data_ptr(),
                                              wt, lw, d, dx.data_ptr(), _stream(dev)))
     return dx
