@@ -86,36 +86,62 @@ struct RowPos {
 // per thread.
 constexpr int kCkptThreads = 256, kCkptUnroll = 4;
 
-// x 16-byte aligned with rows a multiple of 16 bytes apart, D a multiple of V.  FLAT: rows
-// contiguous and D a multiple of 32, so that no row index is needed.
-template <typename T, bool FLAT>
+// How rows of the wide tensor are reached: FLAT, rows contiguous, 16-byte aligned and a multiple of 32
+// values long, so that no row index is needed; ROWS, every row starts and ends at a 16-byte boundary; TAIL,
+// every row starts at one; ANY, one value at a time.
+enum CkptRows { CKPT_FLAT = 0, CKPT_ROWS = 1, CKPT_TAIL = 2, CKPT_ANY = 3 };
+
+template <typename T, int ROWS>
 __global__ void __launch_bounds__(kCkptThreads)
 ckpt_save_kernel(const T* __restrict__ x, long long ldx, long long rows, int D, int nb,
                  int8_t* __restrict__ q, uint8_t* __restrict__ scale)
 {
     constexpr int V = Vec<T>::N, L = kCkptBlock / V;   // L lanes hold a block
+    constexpr int U = ROWS == CKPT_ANY ? 2 : kCkptUnroll;
     pdl_wait();
     const int per_row = nb * L;
     const long long n = rows * per_row;   // a multiple of L: a block's lanes are in or out together
-    const long long u0 = (long long)blockIdx.x * (kCkptThreads * kCkptUnroll) + threadIdx.x;
-    uint4 raw[kCkptUnroll];
-    RowPos pos(FLAT ? 0 : u0, kCkptThreads, per_row);
+    const long long u0 = (long long)blockIdx.x * (kCkptThreads * U) + threadIdx.x;
+    union Values { T t[V]; uint4 u; } raw[U];
+    RowPos pos(ROWS == CKPT_FLAT ? 0 : u0, kCkptThreads, per_row);
 #pragma unroll
-    for (int i = 0; i < kCkptUnroll; ++i) {
+    for (int i = 0; i < U; ++i) {
         const long long u = u0 + i * kCkptThreads;
-        raw[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (FLAT) {
-            if (u < n) raw[i] = ldg_stream(x + u * V);
+        raw[i].u = make_uint4(0u, 0u, 0u, 0u);
+        if (ROWS == CKPT_FLAT) {
+            if (u < n) raw[i].u = ldg_stream(x + u * V);
         } else {
-            if (u < n && pos.at * V < D) raw[i] = ldg_stream(x + pos.row * ldx + pos.at * V);
+            const int c = pos.at * V;
+            const T* p = x + pos.row * ldx + c;
+            if (ROWS == CKPT_ANY) {
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (u < n && c + j < D) raw[i].t[j] = p[j];
+            } else if (u < n && c + V <= D) {
+                raw[i].u = ldg_stream(p);
+            }
             pos.advance();
         }
     }
+    if (ROWS == CKPT_TAIL) {   // the vectors that a row's end cuts, after the others are on their way
+        RowPos tail(u0, kCkptThreads, per_row);
 #pragma unroll
-    for (int i = 0; i < kCkptUnroll; ++i) {
+        for (int i = 0; i < U; ++i) {
+            const int c = tail.at * V;
+            if (u0 + i * kCkptThreads < n && c < D && c + V > D) {
+                const T* p = x + tail.row * ldx + c;
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (c + j < D) raw[i].t[j] = p[j];
+            }
+            tail.advance();
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
         const long long u = u0 + i * kCkptThreads;
         float v[V];
-        Vec<T>::widen(raw[i], v);
+        Vec<T>::widen(raw[i].u, v);
         uint32_t a = 0u;
 #pragma unroll
         for (int j = 0; j < V; ++j) a = max(a, __float_as_uint(v[j]) & 0x7fffffffu);
@@ -130,37 +156,6 @@ ckpt_save_kernel(const T* __restrict__ x, long long ldx, long long rows, int D, 
             else
                 *reinterpret_cast<uint32_t*>(q + u * V) = ckpt_quant4(v, inv, byte);
             if ((threadIdx.x & (L - 1)) == 0) scale[u / L] = (uint8_t)byte;
-        }
-    }
-    pdl_launch_dependents();
-}
-
-// Any row start and stride: a warp takes kCkptUnroll blocks at a time, lane = column.
-template <typename T>
-__global__ void __launch_bounds__(kCkptThreads)
-ckpt_save_any_kernel(const T* __restrict__ x, long long ldx, long long rows, int D, int nb,
-                     int8_t* __restrict__ q, uint8_t* __restrict__ scale)
-{
-    pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const long long n = rows * nb;
-    const long long b0 = ((long long)blockIdx.x * (kCkptThreads / 32) + (threadIdx.x >> 5)) * kCkptUnroll;
-    RowPos pos(b0, 1, nb);
-    float v[kCkptUnroll];
-#pragma unroll
-    for (int i = 0; i < kCkptUnroll; ++i) {
-        const int c = pos.at * kCkptBlock + lane;
-        v[i] = (b0 + i < n && c < D) ? to_float(x[pos.row * ldx + c]) : 0.f;
-        pos.advance();
-    }
-#pragma unroll
-    for (int i = 0; i < kCkptUnroll; ++i) {
-        const uint32_t a = __reduce_max_sync(0xffffffffu, __float_as_uint(v[i]) & 0x7fffffffu);
-        const int byte = ckpt_scale_byte(a);
-        const float w[4] = {v[i], 0.f, 0.f, 0.f};
-        if (b0 + i < n) {
-            q[(b0 + i) * kCkptBlock + lane] = (int8_t)ckpt_quant4(w, ckpt_inv_step(byte), byte);
-            if (lane == 0) scale[b0 + i] = (uint8_t)byte;
         }
     }
     pdl_launch_dependents();
@@ -185,8 +180,8 @@ __device__ __forceinline__ uint4 ckpt_pack(const float* f)
     return o.u;
 }
 
-// y 16-byte aligned, D a multiple of V.  FLAT: D a multiple of 32.
-template <typename T, bool FLAT>
+// y [rows][D] contiguous and 16-byte aligned.  FLAT: D a multiple of 32; ROWS: of V.
+template <typename T, int ROWS>
 __global__ void __launch_bounds__(kCkptThreads)
 ckpt_load_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ scale, long long rows,
                  int D, int nb, T* __restrict__ y)
@@ -209,7 +204,7 @@ ckpt_load_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ scale
             byte[i] = __ldg(scale + u / L);
         }
     }
-    RowPos pos(FLAT ? 0 : u0, kCkptThreads, per_row);
+    RowPos pos(ROWS == CKPT_FLAT ? 0 : u0, kCkptThreads, per_row);
 #pragma unroll
     for (int i = 0; i < kCkptUnroll; ++i) {
         const long long u = u0 + i * kCkptThreads;
@@ -219,7 +214,7 @@ ckpt_load_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ scale
         const float step = ckpt_step(byte[i]);
 #pragma unroll
         for (int j = 0; j < V; ++j) f[j] *= step;
-        if (FLAT) {
+        if (ROWS == CKPT_FLAT) {
             if (u < n) *reinterpret_cast<uint4*>(y + u * V) = ckpt_pack<T>(f);
         } else {
             if (u < n && pos.at * V < D) *reinterpret_cast<uint4*>(y + pos.row * D + pos.at * V) = ckpt_pack<T>(f);
@@ -229,24 +224,59 @@ ckpt_load_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ scale
     pdl_launch_dependents();
 }
 
+// Any D: a thread makes one 16-byte vector of the flat y, wherever its V values start in a row, from the
+// aligned words of q that hold them, so that every store is whole (stores of single values would each
+// touch a sector: 8 times the write traffic).  A vector that spans two rows goes value by value.
 template <typename T>
 __global__ void __launch_bounds__(kCkptThreads)
 ckpt_load_any_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ scale, long long rows,
                      int D, int nb, T* __restrict__ y)
 {
+    constexpr int V = Vec<T>::N;
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const long long n = rows * nb;
-    const long long b0 = ((long long)blockIdx.x * (kCkptThreads / 32) + (threadIdx.x >> 5)) * kCkptUnroll;
-    float v[kCkptUnroll];
-#pragma unroll
-    for (int i = 0; i < kCkptUnroll; ++i)
-        v[i] = b0 + i < n ? (float)q[(b0 + i) * kCkptBlock + lane] * ckpt_step(__ldg(scale + b0 + i)) : 0.f;
-    RowPos pos(b0, 1, nb);
+    const long long total = rows * D;
+    const long long f0 = ((long long)blockIdx.x * (kCkptThreads * kCkptUnroll) + threadIdx.x) * V;
+    RowPos pos(f0, kCkptThreads * V, D);
 #pragma unroll
     for (int i = 0; i < kCkptUnroll; ++i) {
-        const int c = pos.at * kCkptBlock + lane;
-        if (b0 + i < n && c < D) y[pos.row * D + c] = ckpt_value<T>(v[i]);
+        const long long at = f0 + (long long)i * kCkptThreads * V;
+        const int c = pos.at;
+        float f[8];
+        if (at < total && c + V <= D) {
+            const int8_t* p = q + pos.row * nb * kCkptBlock + c;
+            const uint8_t* s = scale + pos.row * nb;
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(p - (c & 3));
+            const int sh = 8 * (c & 3);
+            uint32_t lo = __ldg(w);
+#pragma unroll
+            for (int j = 0; j < V; j += 4) {
+                // the next word holds values of this vector, or (sh = 0, the last time) is not read
+                const uint32_t hi = sh || j + 4 < V ? __ldg(w + j / 4 + 1) : 0u;
+                ckpt_unpack4(__funnelshift_r(lo, hi, sh), f + j);
+                lo = hi;
+            }
+            const int first = kCkptBlock - (c & (kCkptBlock - 1));   // values in the first block
+            const float s0 = ckpt_step(__ldg(s + c / kCkptBlock)), s1 = ckpt_step(__ldg(s + (c + V - 1) / kCkptBlock));
+#pragma unroll
+            for (int j = 0; j < V; ++j) f[j] *= j < first ? s0 : s1;
+        } else {
+            long long r = pos.row;
+            int k = c;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                f[j] = 0.f;
+                if (at + j < total)
+                    f[j] = (float)q[r * nb * kCkptBlock + k] * ckpt_step(__ldg(scale + r * nb + k / kCkptBlock));
+                if (++k == D) { k = 0; ++r; }
+            }
+        }
+        if (at + V <= total) {
+            *reinterpret_cast<uint4*>(y + at) = ckpt_pack<T>(f);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (at + j < total) y[at + j] = ckpt_value<T>(f[j]);
+        }
         pos.advance();
     }
     pdl_launch_dependents();

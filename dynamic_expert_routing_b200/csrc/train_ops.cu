@@ -218,19 +218,9 @@ beam_status_t beam_balance_backward(const void* logits, int32_t dtype, int32_t T
 // ---------------------------------------------------------------- 8-bit checkpoints
 }  // extern "C"
 
-// Whether every row splits into whole 16-byte vectors.
-template <typename T>
-static bool vector_rows(const void* x, long long ld, int d)
+static dim3 ckpt_grid(long long units, int unroll)
 {
-    return !misaligned(x, 16) && d % Vec<T>::N == 0 && ld % Vec<T>::N == 0;
-}
-
-// One unit per thread and step: a 16-byte vector (vec), or the lanes of one block each.
-template <typename T>
-static dim3 ckpt_grid(long long rows, int nb, bool vec)
-{
-    const long long threads = rows * nb * (vec ? kCkptBlock / Vec<T>::N : 32);
-    return dim3((unsigned)ceil_div(threads, kCkptThreads * kCkptUnroll));
+    return dim3((unsigned)ceil_div(units, kCkptThreads * unroll));
 }
 
 extern "C" {
@@ -246,11 +236,14 @@ beam_status_t beam_checkpoint_save(const void* x, int32_t dtype, int64_t rows, i
     const int nb = (int)ceil_div(d, kCkptBlock);
     BEAM_HOST_CUDA(with_type3(dtype, [&](auto z) {
         using T = decltype(z);
-        auto kernel = ckpt_save_any_kernel<T>;
-        if (vector_rows<T>(x, ld_x, d))
-            kernel = ld_x == d && d % kCkptBlock == 0 ? ckpt_save_kernel<T, true> : ckpt_save_kernel<T, false>;
-        return launch_free(kernel, ckpt_grid<T>(rows, nb, kernel != ckpt_save_any_kernel<T>), dim3(kCkptThreads), 0, st,
-                           (const T*)x, (long long)ld_x, (long long)rows, d, nb, q, scale);
+        constexpr int V = Vec<T>::N;
+        const bool aligned = !misaligned(x, 16) && ld_x % V == 0;
+        auto kernel = !aligned                           ? ckpt_save_kernel<T, CKPT_ANY>
+                      : ld_x == d && d % kCkptBlock == 0 ? ckpt_save_kernel<T, CKPT_FLAT>
+                      : d % V == 0                       ? ckpt_save_kernel<T, CKPT_ROWS>
+                                                         : ckpt_save_kernel<T, CKPT_TAIL>;
+        return launch_free(kernel, ckpt_grid(rows * nb * (kCkptBlock / V), aligned ? kCkptUnroll : 2), dim3(kCkptThreads),
+                           0, st, (const T*)x, (long long)ld_x, (long long)rows, d, nb, q, scale);
     }));
     return BEAM_OK;
 }
@@ -261,15 +254,19 @@ beam_status_t beam_checkpoint_load(const int8_t* q, const uint8_t* scale, int64_
     beam_host_clear_error();
     TRY(check_ckpt(q, scale, rows, d));
     TRY(check_matrix("y", y, dtype, true, rows, d, d));
+    if (misaligned(y, 16)) FAIL_ARG("y must be 16-byte aligned");
     if (rows == 0) return BEAM_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int nb = (int)ceil_div(d, kCkptBlock);
     BEAM_HOST_CUDA(with_type3(dtype, [&](auto z) {
         using T = decltype(z);
-        auto kernel = ckpt_load_any_kernel<T>;
-        if (vector_rows<T>(y, d, d)) kernel = d % kCkptBlock == 0 ? ckpt_load_kernel<T, true> : ckpt_load_kernel<T, false>;
-        return launch_free(kernel, ckpt_grid<T>(rows, nb, kernel != ckpt_load_any_kernel<T>), dim3(kCkptThreads), 0, st, q,
-                           scale, (long long)rows, d, nb, (T*)y);
+        constexpr int V = Vec<T>::N;
+        auto kernel = d % kCkptBlock == 0 ? ckpt_load_kernel<T, CKPT_FLAT>
+                      : d % V == 0        ? ckpt_load_kernel<T, CKPT_ROWS>
+                                          : ckpt_load_any_kernel<T>;
+        const long long units = d % V == 0 ? rows * nb * (kCkptBlock / V) : ceil_div(rows * d, V);
+        return launch_free(kernel, ckpt_grid(units, kCkptUnroll), dim3(kCkptThreads), 0, st, q, scale, (long long)rows, d,
+                           nb, (T*)y);
     }));
     return BEAM_OK;
 }

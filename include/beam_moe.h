@@ -548,8 +548,8 @@ beam_status_t beam_balance_backward(const void *logits_dev, int32_t dtype, int32
  * q 2^k, off by at most 2^(k-1) (k = 122 limits |q| to 63, so that no value passes float32's
  * range).  A block with an infinity or a NaN gets the byte 255 and reads back as NaN.
  * beam_checkpoint_save: x_dev [rows][d], rows ld_x elements apart, float32, bfloat16 or float16.
- * beam_checkpoint_load: y_dev [rows][d] contiguous, of any of the three types (float16 values
- *   past 65504 saturate).
+ * beam_checkpoint_load: y_dev [rows][d] contiguous and 16-byte aligned, of any of the three types
+ *   (float16 values past 65504 saturate).
  * d <= 65536.  The callers of q and scale never change them, so one checkpoint serves any
  * number of backward calls.
  */
