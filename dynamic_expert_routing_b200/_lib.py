@@ -127,10 +127,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.beam_router_weight_grad_workspace.argtypes = [I, I, I]
     lib.beam_router_weight_grad_workspace.restype = Q
     lib.beam_router_weight_grad.argtypes = [P, P, I, I, P, I, Q, I, I, P, P, Q, P]
-    lib.beam_router_input_grad.argtypes = [P, I, Q, I, I, P, I, Q, I, P, P]
+    lib.beam_router_input_grad.argtypes = [P, I, Q, I, I, P, I, Q, I, P, Q, P]
+    lib.beam_moe_checkpoint.argtypes = [P, I, P, P, P, P, P, P, P]
+    lib.beam_moe_router_input_grad.argtypes = [P, P, Q, I, P, Q, P]
     for f in (lib.beam_balance_forward, lib.beam_balance_backward, lib.beam_checkpoint_save,
               lib.beam_checkpoint_load, lib.beam_checkpoint_route_grad,
-              lib.beam_router_weight_grad, lib.beam_router_input_grad):
+              lib.beam_router_weight_grad, lib.beam_router_input_grad, lib.beam_moe_checkpoint,
+              lib.beam_moe_router_input_grad):
         f.restype = ctypes.c_int
     lib.beam_softtopk_forward.restype = ctypes.c_int
     lib.beam_softtopk_backward.restype = ctypes.c_int

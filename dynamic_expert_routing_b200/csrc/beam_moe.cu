@@ -31,6 +31,7 @@
 #include "decode_fused.cuh"
 #include "route_grad.cuh"
 #include "softtopk.cuh"
+#include "ckpt_handle.cuh"
 
 using namespace beam;
 
@@ -241,6 +242,8 @@ struct beam_moe {
     // gradient), the per-pair logit gradients and the dW partial columns
     bool last_train = false;
     YOut last_yr;
+    int l_splits = 1;             // K slices of the last forward's router logits, l_stride apart
+    long long l_stride = 0;
     float2* pair_grad = nullptr;  // [Tmax*K] (d_gate_logit, d_mask_logit) of routed rows, at
                                   // each pair's position in perm
     int dw_chunks = 0;            // column chunks of the dW pass (32 vectors of x each)
@@ -264,6 +267,8 @@ struct beam_moe {
     YOut ep_ysh;
     bool ep_fork = false;
     YOut g_yr;           // Y_perm of the captured forward
+    int g_lsplits = 1;   // the captured forward's l_splits and l_stride
+    long long g_lstride = 0;
     // launch accounting and optional per-stage timing
     long long launches = 0;
     bool prof = false;
@@ -1119,6 +1124,8 @@ static beam_status_t forward_impl(beam_moe* h, const T* x, int T_, float* y, uin
     } else {
         BEAM_CUDA(launch_router_gemv<T>(h, x, S, Tr, D, (const T*)h->wrm, h->n2E, h->ldL, h->L, st));
     }
+    h->l_splits = lsplits;
+    h->l_stride = lstride;
     // 2-3. routing decision and compaction.  Small batches (one 32-token chunk) run them as one
     // single-CTA kernel; larger ones as select -> bit planes -> scan -> scatter + gather.
     cudaError_t e;
@@ -2274,6 +2281,8 @@ static beam_status_t forward_entry(beam_moe* h, const void* x, int32_t T, float*
             h->launches += h->g_kernels;
             h->cur = rin ? *rin : own_routing(h);
             h->last_yr = h->g_yr;
+            h->l_splits = h->g_lsplits;
+            h->l_stride = h->g_lstride;
         } else {
             bool captured = false;
             if (graphable) {
@@ -2300,6 +2309,8 @@ static beam_status_t forward_entry(beam_moe* h, const void* x, int32_t T, float*
                         h->g_rin = rin ? *rin : RouteIn();
                         h->g_kernels = (int)nn;
                         h->g_yr = h->last_yr;
+                        h->g_lsplits = h->l_splits;
+                        h->g_lstride = h->l_stride;
                         captured = true;
                     }
                     if (g) cudaGraphDestroy(g);
@@ -2595,6 +2606,56 @@ beam_status_t beam_moe_backward_router(beam_moe_t* h, const void* x, const float
     else
         BEAM_TRY(backward_impl<float>(h, static_cast<const float*>(x), dy, T, reg_scale, dw_router,
                                       dw_mask, dx, d_gate_logit, d_mask_logit, dghat, st));
+    return BEAM_OK;
+}
+
+// ---------------------------------------------------------------- checkpoint of a training forward
+beam_status_t beam_moe_checkpoint(beam_moe_t* h, int32_t T, int8_t* y_q, uint8_t* y_scale, int32_t* topk_id,
+                                  float* gate, float* mask_logit, float* logits, void* stream)
+{
+    g_err[0] = 0;
+    if (!h) return fail(BEAM_ERR_INVALID_ARG, "handle is NULL");
+    if (h->Ew == 0)
+        return fail(BEAM_ERR_UNSUPPORTED, "a routing-only handle (beam_moe_create_ep) has no expert outputs to keep");
+    if (T < 0 || T > h->Tmax) return fail(BEAM_ERR_INVALID_ARG, "T=%d outside [0, %d]", T, h->Tmax);
+    if (T == 0) return BEAM_OK;
+    if (!h->last_train || h->last_T != T)
+        return fail(BEAM_ERR_NO_FORWARD, "a checkpoint needs the handle's last forward to be a BEAM_TRAIN forward "
+                    "of the same T (last forward: T=%d, %s)", h->last_T, h->last_train ? "training" : "not training");
+    if (!y_q || !y_scale || !topk_id || !gate || !mask_logit)
+        return fail(BEAM_ERR_INVALID_ARG, "y_q, y_scale, topk_id, gate and mask_logit are required");
+    if (reinterpret_cast<uintptr_t>(y_q) & 15) return fail(BEAM_ERR_INVALID_ARG, "y_q must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(topk_id) | reinterpret_cast<uintptr_t>(gate) |
+         reinterpret_cast<uintptr_t>(mask_logit) | reinterpret_cast<uintptr_t>(logits)) & 3)
+        return fail(BEAM_ERR_INVALID_ARG, "the int32 and float32 outputs must be 4-byte aligned");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const long long rows = (long long)T * h->K;
+    const int nb = ceil_div(h->D, kCkptBlock);
+    const dim3 grid((unsigned)ceil_div(rows * nb * (kCkptBlock / 4), kCkptThreads * kCkptHandleUnroll));
+    const YOut& yr = h->last_yr;
+    BEAM_CUDA(yr.f16 ? launch_free(ckpt_experts_kernel<__half>, grid, dim3(kCkptThreads), 0, st, (const __half*)yr.base,
+                                   yr.splits, yr.stride, (const int*)h->inv, rows, h->D, nb, y_q, y_scale)
+                     : launch_free(ckpt_experts_kernel<float>, grid, dim3(kCkptThreads), 0, st, (const float*)yr.base,
+                                   yr.splits, yr.stride, (const int*)h->inv, rows, h->D, nb, y_q, y_scale));
+    BEAM_CUDA(cudaMemcpyAsync(topk_id, h->topk_id, rows * 4, cudaMemcpyDeviceToDevice, st));
+    BEAM_CUDA(cudaMemcpyAsync(gate, h->gate, rows * 4, cudaMemcpyDeviceToDevice, st));
+    BEAM_CUDA(cudaMemcpyAsync(mask_logit, h->mlogit, rows * 4, cudaMemcpyDeviceToDevice, st));
+    if (logits) {
+        const long long Tr = ceil_div(T, h->S);
+        BEAM_CUDA(launch_free(ckpt_logits_kernel, dim3((unsigned)ceil_div(Tr * h->n2E, 256)), dim3(256), 0, st,
+                              (const float*)h->L, h->l_splits, h->l_stride, h->ldL, Tr, h->n2E, logits));
+    }
+    // the handle's buffers are read until here: a destroy waits for it
+    BEAM_CUDA(cudaEventRecord(h->done, st));
+    return BEAM_OK;
+}
+
+beam_status_t beam_moe_router_input_grad(beam_moe_t* h, const float* dlogits, int64_t ld_dlogits, int32_t T, float* dx,
+                                         int64_t ld_dx, void* stream)
+{
+    g_err[0] = 0;
+    if (!h) return fail(BEAM_ERR_INVALID_ARG, "handle is NULL");
+    BEAM_TRY(beam_host_input_grad_rows(dlogits, ld_dlogits, T, h->n2E, h->wrm, h->cfg.dtype, h->D, h->D, dx, ld_dx, stream));
     return BEAM_OK;
 }
 

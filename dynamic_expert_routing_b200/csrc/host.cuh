@@ -16,6 +16,12 @@ BEAM_HIDDEN beam_status_t beam_host_fail(beam_status_t st, const char* fmt, ...)
 BEAM_HIDDEN void beam_host_clear_error();
 BEAM_HIDDEN void beam_host_trace(const char* fmt, ...) __attribute__((format(printf, 1, 2)));
 
+// dx [T][d] (rows ld_dx apart) = dlogits [T][C] W^T for W^T given as its rows, w [C][ld_w] (a layer's
+// repacked router): beam_router_input_grad with the other order of W.
+BEAM_HIDDEN beam_status_t beam_host_input_grad_rows(const float* dlogits, int64_t ld_dlogits, int32_t T, int32_t C,
+                                                    const void* w, int32_t w_dtype, int64_t ld_w, int32_t d,
+                                                    float* dx, int64_t ld_dx, void* stream);
+
 #define BEAM_HOST_CUDA(call)                                                              \
     do {                                                                                  \
         cudaError_t e_ = (call);                                                          \

@@ -443,6 +443,31 @@ static beam_status_t check_linear(int T, int C, int d, const void* g, int dtype,
     return check_matrix("dlogits", g, dtype, false, T, C, ldg);
 }
 
+static beam_status_t check_dx(const float* dx, int T, int d, long long ld_dx)
+{
+    if ((T > 0 && !dx) || misaligned(dx, 4)) FAIL_ARG("dx must be a 4-byte aligned pointer");
+    if (ld_dx < d || ld_dx > (1LL << 31) - 1) FAIL_ARG("dx: row stride %lld is below its %d columns, or too long", ld_dx, d);
+    return BEAM_OK;
+}
+
+beam_status_t beam_host_input_grad_rows(const float* dlogits, int64_t ld_dlogits, int32_t T, int32_t C, const void* w,
+                                        int32_t w_dtype, int64_t ld_w, int32_t d, float* dx, int64_t ld_dx, void* stream)
+{
+    TRY(check_linear(T, C, d, dlogits, BEAM_DTYPE_F32, ld_dlogits));
+    TRY(check_dx(dx, T, d, ld_dx));
+    if (T == 0) return BEAM_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    lin::Params p = lin_params(T, d, C);
+    p.a = operand(dlogits, BEAM_DTYPE_F32, ld_dlogits, C);
+    p.b = operand(w, w_dtype, ld_w, d);
+    p.out = dx;
+    p.cp = (int)ld_dx;
+    const int pairs = std::max(1, num_sms() / 2);
+    BEAM_HOST_CUDA((w_dtype == BEAM_DTYPE_F32 ? launch_rows<lin::SRC_F32, false, lin::SRC_F32, true>(p, pairs, st)
+                                              : launch_rows<lin::SRC_F32, false, lin::SRC_BF16, true>(p, pairs, st)));
+    return BEAM_OK;
+}
+
 extern "C" {
 
 int64_t beam_router_weight_grad_workspace(int32_t T, int32_t d, int32_t C)
@@ -490,19 +515,19 @@ beam_status_t beam_router_weight_grad(const int8_t* q, const uint8_t* scale, int
 
 beam_status_t beam_router_input_grad(const void* dlogits, int32_t dtype, int64_t ld_dlogits, int32_t T, int32_t C,
                                      const void* w, int32_t w_dtype, int64_t ld_w, int32_t d, float* dx,
-                                     void* stream)
+                                     int64_t ld_dx, void* stream)
 {
     beam_host_clear_error();
     TRY(check_linear(T, C, d, dlogits, dtype, ld_dlogits));
     TRY(check_matrix("w", w, w_dtype, false, d, C, ld_w));
-    if ((T > 0 && !dx) || misaligned(dx, 4)) FAIL_ARG("dx must be a 4-byte aligned pointer");
+    TRY(check_dx(dx, T, d, ld_dx));
     if (T == 0) return BEAM_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     lin::Params p = lin_params(T, d, C);
     p.a = operand(dlogits, dtype, ld_dlogits, C);
     p.b = operand(w, w_dtype, ld_w, C);
     p.out = dx;
-    p.cp = d;
+    p.cp = (int)ld_dx;
     const int pairs = std::max(1, num_sms() / 2);
     const bool g32 = dtype == BEAM_DTYPE_F32, w32 = w_dtype == BEAM_DTYPE_F32;
     const cudaError_t e =

@@ -14,6 +14,8 @@ from . import _lib
 from ._lib import (BEAM_DTYPE_BF16, BEAM_DTYPE_F32, BEAM_MASK_OFF, BEAM_FUSED_DECODE, BEAM_NO_GRAPH,
                    BEAM_PATH_STREAM, BEAM_PATH_TENSOR, BEAM_TRAIN, BeamConfig, BeamGenConfig,
                    BeamRouting, BeamStats, BeamWeights, check)
+from .training import (CKPT_BLOCK, balance_loss_backward, checkpoint_route_grad, checkpoint_save,
+                       router_weight_grad)
 
 _DTYPES = {torch.float32: BEAM_DTYPE_F32, torch.bfloat16: BEAM_DTYPE_BF16}
 _PATHS = {None: 0, "auto": 0, "stream": BEAM_PATH_STREAM, "tensor": BEAM_PATH_TENSOR}
@@ -126,6 +128,68 @@ class BeamMoE:
             _ptr(out.get("d_mask_logit")), _ptr(out.get("dghat")),
             ctypes.c_void_p(_stream_handle(stream))))
         return out
+
+    def checkpoint(self, x: torch.Tensor, stream=None) -> dict:
+        """The state of the last forward(x, train=True) in 8 bits per activation, so that its backward
+        can follow later, after other forwards of this layer: x and y, 8-bit checkpoints of the
+        routed rows of x [rows][D] and of every slot's expert output [T K][D] (training.checkpoint_load
+        reads them back), the routing topk_id, gate and mask_logit [T][K], and the routed rows' logits
+        [rows][2E] float32 (the first E columns are balance_loss's input).  rows = T, or one per
+        segment.  See beam_moe_checkpoint."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.checkpoint(x)
+        if not (x.is_cuda and x.is_contiguous() and x.dtype == self.dtype and x.dim() == 2
+                and x.shape[1] == self.d_model):
+            raise ValueError("x must be a contiguous [T][D] CUDA tensor of the layer's storage dtype")
+        T, K, E, D = x.shape[0], self.top_k, self.n_experts, self.d_model
+        S, nb, dev = max(1, self.cfg.segment_len), -(-D // CKPT_BLOCK), x.device
+        rows = -(-T // S)
+        y = dict(q=torch.empty(T * K, nb * CKPT_BLOCK, dtype=torch.int8, device=dev),
+                 scale=torch.empty(T * K, nb, dtype=torch.uint8, device=dev), d=D)
+        out = dict(y=y, topk_id=torch.empty(T, K, dtype=torch.int32, device=dev),
+                   gate=torch.empty(T, K, dtype=torch.float32, device=dev),
+                   mask_logit=torch.empty(T, K, dtype=torch.float32, device=dev),
+                   logits=torch.empty(rows, 2 * E, dtype=torch.float32, device=dev))
+        check(_lib.load().beam_moe_checkpoint(self._h, T, y["q"].data_ptr(), y["scale"].data_ptr(),
+                                              out["topk_id"].data_ptr(), out["gate"].data_ptr(),
+                                              out["mask_logit"].data_ptr(), out["logits"].data_ptr(),
+                                              _stream_handle(None)))
+        out["x"] = checkpoint_save(x[::S])
+        return out
+
+    def backward_checkpoint(self, ckpt: dict, dy: torch.Tensor, reg_scale: float = 0.0,
+                            balance: dict | None = None, balance_scale: float = 0.0,
+                            valid: torch.Tensor | None = None, cu_seqlens: torch.Tensor | None = None,
+                            stream=None) -> dict:
+        """backward_router from a checkpoint(), for the upstream gradient dy [T][D] (float32 or
+        bfloat16) and reg_scale = dL/dL_reg, plus balance_scale = dL/dL_bal times the gradient of
+        balance_loss(ckpt["logits"][:, :E], topk_id of the routed rows, valid, cu_seqlens), whose
+        result is `balance`.  Returns dw_router, dw_mask [D][E], dx [T][D] (float32; with segments 0
+        but for the routed rows) and the per-slot dghat, d_gate_logit and d_mask_logit [T][K]."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.backward_checkpoint(ckpt, dy, reg_scale, balance, balance_scale, valid,
+                                                cu_seqlens)
+        if balance is None and balance_scale != 0.0:
+            raise ValueError("balance_scale needs the balance loss's result")
+        T, E, D, S = dy.shape[0], self.n_experts, self.d_model, max(1, self.cfg.segment_len)
+        slots = checkpoint_route_grad(ckpt["y"], ckpt["gate"], ckpt["mask_logit"], dy, reg_scale,
+                                      self.cfg.segment_len)
+        ids, gr, gl = ckpt["topk_id"], slots["d_gate_logit"], slots["d_mask_logit"]
+        if S > 1:                      # the decisions' rows
+            ids, gr, gl = ids[::S].contiguous(), gr[::S].contiguous(), gl[::S].contiguous()
+        if balance is None:            # no token counts: the slots' terms alone
+            G = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
+            balance = dict(counts=torch.zeros(G, E, dtype=torch.int32, device=dy.device),
+                           tokens=torch.zeros(G, dtype=torch.int32, device=dy.device))
+        g = balance_loss_backward(ckpt["logits"][:, :E], ids, balance, balance_scale, valid, cu_seqlens,
+                                  gr, gl)
+        dw = router_weight_grad(ckpt["x"], g, parts=2)
+        dx = (torch.empty if S == 1 else torch.zeros)(T, D, dtype=torch.float32, device=dy.device)
+        check(_lib.load().beam_moe_router_input_grad(self._h, g.data_ptr(), 2 * E, g.shape[0], dx.data_ptr(),
+                                                     S * D, _stream_handle(None)))
+        return dict(dw_router=dw[0], dw_mask=dw[1], dx=dx, **slots)
 
     def forward_routed(self, x: torch.Tensor, routing: dict, path: str | None = None,
                        out: torch.Tensor | None = None, stream=None, graph: bool = True) -> torch.Tensor:

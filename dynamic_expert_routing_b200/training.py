@@ -238,5 +238,5 @@ def router_input_grad(dlogits: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
         raise ValueError(f"w must have dlogits' {C} columns")
     dx = torch.empty(T, d, dtype=torch.float32, device=dev)
     check(_lib.load().beam_router_input_grad(dlogits.data_ptr(), dt, ld, T, C, w.data_ptr(),
-                                             wt, lw, d, dx.data_ptr(), _stream(dev)))
+                                             wt, lw, d, dx.data_ptr(), d, _stream(dev)))
     return dx

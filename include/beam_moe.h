@@ -582,8 +582,8 @@ beam_status_t beam_checkpoint_route_grad(const int8_t *q_dev, const uint8_t *sca
  *   [W_r | W_m], parts = L the L layers of a mask generator.  T = 0 writes zeros.  workspace_dev:
  *   scratch of beam_router_weight_grad_workspace(T, d, C) bytes (0 for many shapes), 16-byte
  *   aligned, free again when the call's kernels are done.
- * beam_router_input_grad: dx_dev [T][d] float32 = dlogits W^T, w_dev [d][C] float32 or bfloat16,
- *   rows ld_w elements apart.
+ * beam_router_input_grad: dx_dev [T][d] float32, rows ld_dx elements apart, = dlogits W^T, w_dev [d][C]
+ *   float32 or bfloat16, rows ld_w elements apart.
  * A dlogits or W value that is not finite makes the outputs it reaches NaN.  Both run on the
  * tensor cores with float32 accuracy; a bounded device wait that runs out sets the outputs to NaN.
  */
@@ -595,7 +595,29 @@ beam_status_t beam_router_weight_grad(const int8_t *q_dev, const uint8_t *scale_
                                       void *stream);
 beam_status_t beam_router_input_grad(const void *dlogits_dev, int32_t dtype, int64_t ld_dlogits,
                                      int32_t T, int32_t C, const void *w_dev, int32_t w_dtype,
-                                     int64_t ld_w, int32_t d, float *dx_dev, void *stream);
+                                     int64_t ld_w, int32_t d, float *dx_dev, int64_t ld_dx,
+                                     void *stream);
+
+/*
+ * Checkpoint of a layer's training forward: what beam_moe_backward_router reads of the handle, written to
+ * the caller's buffers, so that the handle can run other forwards (more micro-batches, other steps of a
+ * pipeline) before this one's backward.  Needs the handle's last forward to be a BEAM_TRAIN forward of
+ * the same T (else BEAM_ERR_NO_FORWARD).  Writes
+ *   y_q_dev [T K][D rounded up to 32], y_scale_dev [T K][ceil(D / 32)]: the expert outputs of every
+ *   (token, slot) as an 8-bit checkpoint (beam_checkpoint_save's format), row t K + k = slot k;
+ *   topk_id_dev, gate_dev, mask_logit_dev [T][K]: the routing (beam_moe_get_routing's, on the device);
+ *   logits_dev (optional) [ceil(T / segment_len)][2E] float32: the routed rows' logits x [W_r | W_m].
+ * The input x is not part of it: beam_checkpoint_save keeps the routed rows of x.  The backward is then
+ * beam_checkpoint_route_grad, beam_balance_backward (the joined logit gradient, [rows][2E]),
+ * beam_router_weight_grad with parts = 2, and beam_moe_router_input_grad:
+ *   dx_dev [T][D] float32, rows ld_dx elements apart, = dlogits [W_r | W_m]^T with the handle's own
+ *   router matrices, for dlogits_dev [T][2E] float32, rows ld_dlogits elements apart.
+ */
+beam_status_t beam_moe_checkpoint(beam_moe_t *h, int32_t T, int8_t *y_q_dev, uint8_t *y_scale_dev,
+                                  int32_t *topk_id_dev, float *gate_dev, float *mask_logit_dev,
+                                  float *logits_dev, void *stream);
+beam_status_t beam_moe_router_input_grad(beam_moe_t *h, const float *dlogits_dev, int64_t ld_dlogits,
+                                         int32_t T, float *dx_dev, int64_t ld_dx, void *stream);
 
 /* Free every device buffer of the handle (waits for its pending work).  NULL is ignored. */
 void beam_moe_destroy(beam_moe_t *h);

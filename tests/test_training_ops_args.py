@@ -51,6 +51,7 @@ def test_checkpoint_refusals(lib):
     assert lib.beam_checkpoint_load(P, P, 4, 8, None, F32, None) == BAD
     assert lib.beam_checkpoint_load(P, P, 4, 8, P, 7, None) == BAD
     assert lib.beam_checkpoint_load(P + 1, P, 4, 8, P, F32, None) == BAD
+    assert lib.beam_checkpoint_load(P, P, 4, 8, P + 4, F32, None) == BAD
     # nothing to do: no CUDA call
     assert save(n=0, x=None, q=None, s=None) == 0 and lib.beam_checkpoint_load(None, None, 0, 8, None, F32, None) == 0
 
@@ -62,11 +63,25 @@ def test_gradient_refusals(lib):
                dict(ld=4), dict(seg=-1), dict(seg=65537), dict(reg=float("inf")), dict(out=None), dict(out=P + 2),
                dict(T=1 << 30, K=32)):
         assert rg(**kw) == BAD, kw
-    ig = lambda T=4, C=5, d=8, g=P, dt=F32, ld=5, w=P, wt=F32, lw=5, dx=P: lib.beam_router_input_grad(  # noqa: E731
-        g, dt, ld, T, C, w, wt, lw, d, dx, None)
+    ig = lambda T=4, C=5, d=8, g=P, dt=F32, ld=5, w=P, wt=F32, lw=5, dx=P, lx=8: lib.beam_router_input_grad(  # noqa: E731
+        g, dt, ld, T, C, w, wt, lw, d, dx, lx, None)
     for kw in (dict(T=-1), dict(C=0), dict(C=(1 << 20) + 1, ld=1 << 21, lw=1 << 21), dict(d=0), dict(g=None), dict(g=P + 2), dict(dt=F16),
-               dict(ld=4), dict(w=None), dict(wt=F16), dict(lw=4), dict(dx=None), dict(dx=P + 1)):
+               dict(ld=4), dict(w=None), dict(wt=F16), dict(lw=4), dict(dx=None), dict(dx=P + 1), dict(lx=7),
+               dict(lx=1 << 31)):
         assert ig(**kw) == BAD, kw
+    wg = lambda q=P, T=4, d=8, g=P, dt=F32, ld=6, C=6, parts=1, dw=P: lib.beam_router_weight_grad(  # noqa: E731
+        q, P, T, d, g, dt, ld, C, parts, dw, None, 0, None)
+    for kw in (dict(q=None), dict(q=P + 8), dict(T=-1), dict(d=0), dict(g=None), dict(g=P + 1), dict(dt=F16), dict(ld=5),
+               dict(C=0), dict(parts=0), dict(parts=4), dict(dw=None), dict(dw=P + 2)):
+        assert wg(**kw) == BAD, kw
+    assert lib.beam_router_weight_grad_workspace(-1, 8, 6) == -1
+    assert lib.beam_router_weight_grad_workspace(4, 8, 0) == -1
+    assert lib.beam_router_weight_grad_workspace(0, 8, 6) == 0
+
+
+def test_layer_checkpoint_null_handle(lib):
+    assert lib.beam_moe_checkpoint(None, 1, P, P, P, P, P, None, None) == BAD
+    assert lib.beam_moe_router_input_grad(None, P, 8, 1, P, 8, None) == BAD
 
 
 def test_binding_refuses_host_tensors():
