@@ -148,10 +148,10 @@ balance_partial_kernel(const T* __restrict__ logits, long long ldl, int n_tok, i
     __shared__ float s_w[kBalWarps];
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane % LPR;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;
     const int t0 = (int)min((long long)blockIdx.x * run, (long long)n_tok);
     const int t1 = (int)min((long long)t0 + run, (long long)n_tok);
-    const bool alone = gridDim.x == 1 && !cu;         // one run, one group: finished here
+    const bool alone = gridDim.x == 1 && !cu;         // one run, one group: finished here, without scratch
+    if (!alone && blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;
     const int g_end = cu ? n_seq : 1;
     for (int g = cu ? bal_group_block(cu, n_seq, t0, &s_g) : 0; g < g_end; ++g) {
         const int a = cu ? max(t0, bal_bound(cu, g, n_tok)) : t0;

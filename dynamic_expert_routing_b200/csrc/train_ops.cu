@@ -115,6 +115,7 @@ static BalWork bal_work(int T, int E, int n_seq)
     w.lg = align256(w.n + w.slots * 4);
     w.ticket = align256(w.lg + G * ceil_div(E, 32) * 4);
     w.bytes = w.ticket + 256;
+    if (bal_runs(T, E) == 1 && n_seq == 0) w.bytes = 0;   // finished by its only CTA
     return w;
 }
 
@@ -176,13 +177,13 @@ beam_status_t beam_balance_forward(const void* logits, int32_t dtype, int32_t T,
     if (misaligned(loss, 4) || misaligned(prob, 4) || misaligned(counts, 4) || misaligned(tokens, 4))
         FAIL_ARG("the outputs must be 4-byte aligned");
     const BalWork w = bal_work(T, E, n_seq);
-    if (!workspace || workspace_bytes < w.bytes || misaligned(workspace, 16))
+    if (w.bytes > 0 && (!workspace || workspace_bytes < w.bytes || misaligned(workspace, 16)))
         FAIL_ARG("the workspace must be 16-byte aligned and hold %lld bytes", w.bytes);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
     const BalOut o{loss, prob, counts, tokens};
     BEAM_HOST_CUDA(BAL_DISPATCH(launch_balance, a, ws, w, o, st));
-    if (bal_runs(T, E) == 1 && !cu_seqlens) return BEAM_OK;   // finished by its only CTA
+    if (w.bytes == 0) return BEAM_OK;
     int ep = 1;
     while (ep < std::min(E, 32)) ep *= 2;
     const dim3 grid((unsigned)std::max(1, n_seq), (unsigned)ceil_div(E, 32));

@@ -21,9 +21,17 @@ CKPT_BLOCK = 32   # columns that share a scale
 # microsecond more, and a small call launches in five.)
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 @functools.lru_cache(maxsize=1024)
 def _balance_workspace(T: int, E: int, n_seq: int) -> int:
     return _lib.load().beam_balance_workspace(T, E, n_seq)
+
+
+@functools.lru_cache(maxsize=1024)
+def _weight_grad_workspace(T: int, d: int, C: int, device: int) -> int:
+    return _lib.load().beam_router_weight_grad_workspace(T, d, C)
 
 
 def _on_stream(fn):
@@ -36,9 +44,9 @@ def _on_stream(fn):
             with torch.cuda.stream(stream):
                 return fn(*args, **kw)
         first = args[0] if args else next(iter(kw.values()))
-        t = first["q"] if isinstance(first, dict) else first
-        if t.is_cuda and t.device.index != torch.cuda.current_device():
-            with torch.cuda.device(t.device):
+        index = (first["q"] if isinstance(first, dict) else first).get_device()   # -1 on the host
+        if index >= 0 and index != torch._C._cuda_getDevice():
+            with torch.cuda.device(index):
                 return fn(*args, **kw)
         return fn(*args, **kw)
     return call
@@ -47,7 +55,7 @@ def _on_stream(fn):
 def _stream(device: torch.device) -> int:
     """The handle of the device's current stream (the raw query: torch.cuda.current_stream()
     builds a Stream object, 3 us of a call that launches in 5)."""
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return _raw_stream(device.index)
 
 
 def _matrix(name: str, t: torch.Tensor, dtypes: dict, device=None):
@@ -106,10 +114,11 @@ def balance_loss(logits: torch.Tensor, topk_id: torch.Tensor, valid: torch.Tenso
     prob = torch.empty(G, E, dtype=torch.float32, device=dev)
     counts = torch.empty(G, E, dtype=torch.int32, device=dev)
     tokens = torch.empty(G, dtype=torch.int32, device=dev)
-    ws = torch.empty(max(size, 0), dtype=torch.uint8, device=dev)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev) if size > 0 else None
     check(lib.beam_balance_forward(logits.data_ptr(), dt, T, E, ld, ids, K, v, cu, n,
                                    loss.data_ptr(), prob.data_ptr(), counts.data_ptr(),
-                                   tokens.data_ptr(), ws.data_ptr(), size, _stream(dev)))
+                                   tokens.data_ptr(), None if ws is None else ws.data_ptr(), size,
+                                   _stream(dev)))
     return dict(loss=loss, counts=counts, prob=prob, tokens=tokens)
 
 
@@ -220,7 +229,7 @@ def router_weight_grad(ckpt: dict, dlogits: torch.Tensor, parts: int = 1) -> tor
     f32 = dict(dtype=torch.float32, device=dev)
     dw = torch.empty(d, C, **f32) if parts == 1 else torch.empty(parts, d, C // parts, **f32)
     lib = _lib.load()
-    size = lib.beam_router_weight_grad_workspace(T, d, C)
+    size = _weight_grad_workspace(T, d, C, dev.index)   # the split depends on the device's SMs
     ws = torch.empty(size, dtype=torch.uint8, device=dev) if size > 0 else None
     check(lib.beam_router_weight_grad(q, scale, T, d, dlogits.data_ptr(), dt, ld, C, parts, dw.data_ptr(),
                                       None if ws is None else ws.data_ptr(), size, _stream(dev)))

@@ -510,8 +510,8 @@ beam_status_t beam_softtopk_backward(const float *y_dev, const float *dy_dev, in
  * beam_balance_forward: logits_dev [T][E] of `dtype` (BEAM_DTYPE_F32 or _BF16), rows ld_logits
  *   elements apart -> loss_dev [1], prob_dev [G][E] float32, counts_dev [G][E] int32, tokens_dev
  *   [G] int32 (G = n_seq, or 1).  workspace_dev: scratch of at least
- *   beam_balance_workspace(T, E, n_seq) bytes, 16-byte aligned, free again when the call's
- *   kernels are done.
+ *   beam_balance_workspace(T, E, n_seq) bytes (0 for a small batch), 16-byte aligned, free again
+ *   when the call's kernels are done.
  * beam_balance_backward: the loss's gradient times `scale` for the same inputs and the forward's
  *   counts and tokens (f is a count and carries no gradient),
  *   dlogits_tj = scale / (G' n_g) p_tj (f_gj - sum_i f_gi p_ti),  G' = groups with n_g > 0,

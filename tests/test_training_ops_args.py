@@ -29,14 +29,14 @@ def _balance(lib, x=P, dt=F32, T=4, E=8, ld=8, ids=P, K=2, valid=None, cu=None, 
 def test_balance_refusals(lib):
     for kw in (dict(T=-1), dict(E=0), dict(E=257), dict(K=0), dict(K=33), dict(dt=F16), dict(dt=9), dict(ld=7),
                dict(x=None), dict(x=P + 2), dict(ids=None), dict(ids=P + 1), dict(n=3), dict(cu=P, n=0),
-               dict(cu=P, n=65537), dict(cu=P + 2, n=2), dict(loss=None), dict(loss=P + 1), dict(ws=None),
-               dict(ws=P + 8), dict(size=16)):
+               dict(cu=P, n=65537), dict(cu=P + 2, n=2), dict(loss=None), dict(loss=P + 1), dict(cu=P, n=2, ws=None),
+               dict(cu=P, n=2, ws=P + 8), dict(T=10000, size=16)):
         assert _balance(lib, **kw) == BAD, kw
         assert lib.beam_moe_last_error()
     assert lib.beam_balance_workspace(-1, 8, 0) == -1
     assert lib.beam_balance_workspace(4, 0, 0) == -1
     assert lib.beam_balance_workspace(4, 8, 70000) == -1
-    assert 0 < lib.beam_balance_workspace(4, 8, 0) < lib.beam_balance_workspace(70000, 256, 64)
+    assert 0 == lib.beam_balance_workspace(4, 8, 0) < lib.beam_balance_workspace(4, 8, 1) < lib.beam_balance_workspace(70000, 256, 64)
     back = lambda scale=1.0, gr=None, gl=None, out=P, counts=P: lib.beam_balance_backward(  # noqa: E731
         P, F32, 4, 8, 8, P, 2, None, None, 0, counts, P, scale, gr, gl, out, None)
     assert back(scale=float("nan")) == BAD and back(gr=P) == BAD and back(out=None) == BAD
