@@ -79,6 +79,7 @@ static beam_status_t check_balance(const BalArgs& a)
     if (a.T < 0 || a.T > (1 << 30)) FAIL_ARG("T=%d outside [0, 2^30]", a.T);
     if (a.E < 1 || a.E > kMaxExperts) FAIL_ARG("E=%d must be in [1, %d]", a.E, kMaxExperts);
     if (a.K < 1 || a.K > kMaxSlots) FAIL_ARG("K=%d must be in [1, %d]", a.K, kMaxSlots);
+    if ((long long)a.T * a.K > (1LL << 31) - 1) FAIL_ARG("T*K=%lld assignments are too many for int32 counts", (long long)a.T * a.K);
     if (a.cu ? (a.n_seq < 1 || a.n_seq > 65536) : a.n_seq != 0)
         FAIL_ARG("n_seq=%d: 1 to 65536 sequences with cu_seqlens, 0 without", a.n_seq);
     TRY(check_matrix("logits", a.logits, a.dtype, false, a.T, a.E, a.ldl));
@@ -436,7 +437,7 @@ static long long weight_bytes(const lin::Params& p)
 
 static beam_status_t check_linear(int T, int C, int d, const void* g, int dtype, long long ldg)
 {
-    if (T < 0) FAIL_ARG("T=%d is negative", T);
+    if (T < 0 || T > (1 << 30)) FAIL_ARG("T=%d outside [0, 2^30]", T);
     if (C < 1 || C > kMaxLogits) FAIL_ARG("C=%d must be in [1, %d]", C, kMaxLogits);
     if (d < 1 || d > kMaxWidth) FAIL_ARG("d=%d must be in [1, %d]", d, kMaxWidth);
     if (ceil_div(T, lin::BM) * ceil_div(d, lin::BN) > (1LL << 30))

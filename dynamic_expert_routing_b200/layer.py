@@ -136,8 +136,8 @@ class BeamMoE:
         reads them back), the routing topk_id, gate and mask_logit [T][K], and the routed rows' logits
         [rows][2E] float32 (the first E columns are balance_loss's input).  rows = T, or one per
         segment.  See beam_moe_checkpoint."""
-        if stream is not None:
-            with torch.cuda.stream(stream):
+        if stream is not None or (x.is_cuda and x.device.index != torch.cuda.current_device()):
+            with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(x.device):
                 return self.checkpoint(x)
         if not (x.is_cuda and x.is_contiguous() and x.dtype == self.dtype and x.dim() == 2
                 and x.shape[1] == self.d_model):
@@ -167,8 +167,8 @@ class BeamMoE:
         balance_loss(ckpt["logits"][:, :E], topk_id of the routed rows, valid, cu_seqlens), whose
         result is `balance`.  Returns dw_router, dw_mask [D][E], dx [T][D] (float32; with segments 0
         but for the routed rows) and the per-slot dghat, d_gate_logit and d_mask_logit [T][K]."""
-        if stream is not None:
-            with torch.cuda.stream(stream):
+        if stream is not None or (dy.is_cuda and dy.device.index != torch.cuda.current_device()):
+            with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dy.device):
                 return self.backward_checkpoint(ckpt, dy, reg_scale, balance, balance_scale, valid,
                                                 cu_seqlens)
         if balance is None and balance_scale != 0.0:
