@@ -597,35 +597,37 @@ lin_gemm_kernel(const __grid_constant__ Params p)
             if (!ok)
 #pragma unroll
                 for (int j = 0; j < BN / 2; ++j) sum[j] = __uint_as_float(0x7fffffffu);
-            // 32 x 32 sub-tiles through shared memory (lane = row in, lane = 4 columns out), so that a
-            // store instruction writes four rows' 128 bytes
+            // 32 x 32 sub-tiles through shared memory (lane = row in, so that every store instruction writes
+            // whole rows of a sub-tile: four as 16-byte vectors where the output's rows allow, else one)
             const int m0 = t.m0 + rank * kRowsA + lb, rows = min(32, p.M - m0);
+            float* out = p.out + t.slice * p.slice;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int n = nt * BN + 64 * half + 32 * h + 4 * (lane & 7);
+                const int c0 = nt * BN + 64 * half + 32 * h;
                 __syncwarp();
 #pragma unroll
                 for (int j = 0; j < 32; j += 4)
                     *reinterpret_cast<float4*>(buf32 + lane * kStagePitch + j) =
                         make_float4(sum[32 * h + j], sum[32 * h + j + 1], sum[32 * h + j + 2], sum[32 * h + j + 3]);
                 __syncwarp();
-                if (n >= p.N) continue;
-                const int part = n / p.cp, at = n - part * p.cp;
-                float* out = p.out + t.slice * p.slice + ((long long)part * p.M + m0) * p.cp + at;
-                const float* v = buf32 + 4 * (lane & 7);
-                if (at + 4 <= p.cp && n + 4 <= p.N && (p.cp & 3) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0) {
-                    const int r0 = lane >> 3;
-                    float* o = out + (long long)r0 * p.cp;
+                if ((p.cp & 3) == 0 && (p.N & 3) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0) {
+                    const int n = c0 + 4 * (lane & 7), r0 = lane >> 3;
+                    if (n < p.N) {
+                        const int part = n / p.cp;
+                        float* o = out + ((long long)part * p.M + m0 + r0) * p.cp + (n - part * p.cp);
+                        const float* v = buf32 + 4 * (lane & 7);
 #pragma unroll 4
-                    for (int r = r0; r < rows; r += 4, o += 4 * p.cp)
-                        *reinterpret_cast<float4*>(o) = *reinterpret_cast<const float4*>(v + r * kStagePitch);
+                        for (int r = r0; r < rows; r += 4, o += 4LL * p.cp)
+                            *reinterpret_cast<float4*>(o) = *reinterpret_cast<const float4*>(v + r * kStagePitch);
+                    }
                 } else {
-                    for (int r = lane >> 3; r < rows; r += 4)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)   // the four columns may belong to more than one part
-                            if (n + i < p.N)
-                                p.out[t.slice * p.slice + ((long long)((n + i) / p.cp) * p.M + m0 + r) * p.cp +
-                                      (n + i) % p.cp] = v[r * kStagePitch + i];
+                    const int n = c0 + lane;
+                    if (n < p.N) {
+                        const int part = n / p.cp;
+                        float* o = out + ((long long)part * p.M + m0) * p.cp + (n - part * p.cp);
+#pragma unroll 4
+                        for (int r = 0; r < rows; ++r, o += p.cp) *o = buf32[r * kStagePitch + lane];
+                    }
                 }
             }
         }
