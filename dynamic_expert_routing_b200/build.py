@@ -1,10 +1,13 @@
-"""Build libbeam_moe.so in-tree with nvcc for sm_100a (cross-compiles without a GPU)."""
+"""Build libbeam_moe.so in-tree with nvcc for sm_100a (cross-compiles without a GPU), and the native
+side of training.py, _training.so, with g++ against the installed torch."""
 from __future__ import annotations
 
+import importlib.util
 import os
 import re
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -12,6 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libbeam_moe.so")
 UNITS = [os.path.join(CSRC, f) for f in ("beam_moe.cu", "train_ops.cu")]
 OBJ = os.path.join(HERE, "_build")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(HERE, "_training.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 NVCC_FLAGS = [
@@ -38,7 +43,18 @@ def _older(target: str, files) -> bool:
 
 
 def stale() -> bool:
-    return _older(LIB, sources())
+    return _older(LIB, sources()) or _older(BINDING, _included(BINDING_SRC))
+
+
+def binding_command(out: str) -> list:
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    libs = ("torch_python", "torch", "torch_cpu", "torch_cuda", "c10", "c10_cuda", "dl")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            *[a for p in inc for a in ("-isystem", p)], "-o", out, BINDING_SRC,
+            "-L", os.path.join(torch, "lib"), *["-l" + n for n in libs]]
 
 
 def _included(unit: str):
@@ -71,11 +87,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
             cmd.insert(1, "-Xptxas=-v")
             print(" ".join(cmd), flush=True)
         jobs.append((subprocess.Popen(cmd), cmd, tmp, obj))
+    if force or _older(BINDING, _included(BINDING_SRC)):
+        tmp = BINDING + f".tmp{os.getpid()}"
+        cmd = binding_command(tmp)
+        jobs.append((subprocess.Popen(cmd), cmd, tmp, BINDING))
     failed = [cmd for proc, cmd, _, _ in jobs if proc.wait() != 0]
     if failed:
         raise subprocess.CalledProcessError(1, failed[0])
     for _, _, tmp, obj in jobs:
         os.replace(tmp, obj)
+    if not force and not _older(LIB, objs):
+        return LIB
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.check_call([NVCC, "-shared", "-gencode", "arch=compute_100a,code=sm_100a", "-o", tmp, *objs])
     os.replace(tmp, LIB)
