@@ -142,6 +142,7 @@ balance_partial_kernel(const T* __restrict__ logits, long long ldl, int n_tok, i
     const int t0 = (int)min((long long)blockIdx.x * run, (long long)n_tok);
     const int t1 = (int)min((long long)t0 + run, (long long)n_tok);
     const bool alone = gridDim.x == 1 && !cu;         // one run, one group: finished here, without scratch
+    if (alone) pdl_launch_dependents();
     if (!alone && blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;
     const int g_end = cu ? n_seq : 1;
     for (int g = cu ? bal_group(cu, n_seq, t0) : 0; g < g_end; ++g) {
@@ -209,7 +210,7 @@ balance_partial_kernel(const T* __restrict__ logits, long long ldl, int n_tok, i
         if (e == 0) part_n[slot] = s_n;
         __syncthreads();
     }
-    pdl_launch_dependents();
+    if (!alone) pdl_launch_dependents();
 }
 
 // EP: the power of two that holds min(E, 32); 1024 / EP threads share an expert's slots.  (One CTA per

@@ -356,6 +356,7 @@ static lin::Params lin_params(int M, int N, int K)
     p.k_steps = (int)ceil_div(K, lin::BK);
     p.split_steps = p.k_steps;
     p.units = p.m_tiles * p.n_tiles;
+    p.last = 1;
     return p;
 }
 
@@ -503,6 +504,7 @@ beam_status_t beam_router_weight_grad(const int8_t* q, const uint8_t* scale, int
     p.out = need ? static_cast<float*>(workspace) : dw;
     p.slice = (long long)d * ldp;
     p.cp = need ? ldp : cp;
+    p.last = need == 0;
     const int pairs = std::max(1, num_sms() / 2);
     const cudaError_t e = dtype == BEAM_DTYPE_F32 ? launch_slices<lin::SRC_CKPT, true, lin::SRC_F32, true>(p, pairs, st)
                                                   : launch_slices<lin::SRC_CKPT, true, lin::SRC_BF16, true>(p, pairs, st);
