@@ -39,7 +39,7 @@ namespace beam {
 constexpr int kBalThreads = 256, kBalWarps = kBalThreads / 32;
 constexpr int kBalPer = 8;            // logits per lane
 constexpr int kBalRuns = 296;         // most runs of a large batch: two CTAs per SM
-constexpr int kBalReduceThreads = 1024;
+constexpr int kBalReduceThreads = 512;
 
 // Group bounds [cu[g], cu[g+1]) clamped to the batch; one group [0, T) without cu.
 __device__ __forceinline__ int bal_bound(const int* __restrict__ cu, int g, int T)
@@ -213,7 +213,7 @@ balance_partial_kernel(const T* __restrict__ logits, long long ldl, int n_tok, i
     if (!alone) pdl_launch_dependents();
 }
 
-// EP: the power of two that holds min(E, 32); 1024 / EP threads share an expert's slots.  (One CTA per
+// EP: the power of two that holds min(E, 32); 512 / EP threads share an expert's slots.  (One CTA per
 // group would read all slots through one SM: 600 KB for 16384 tokens of 256 experts.)
 __global__ void __launch_bounds__(kBalReduceThreads)
 balance_reduce_kernel(const float* __restrict__ part_p, const int* __restrict__ part_c,
@@ -238,12 +238,21 @@ balance_reduce_kernel(const float* __restrict__ part_p, const int* __restrict__ 
     const int e = e0 + (tid & (EP - 1)), subs = kBalReduceThreads / EP, sub = tid / EP;
     float sum = 0.f;
     int cnt = 0;
-    if (e < E)
-#pragma unroll 8
-        for (int c = c0 + sub; c < c1; c += subs) {
-            sum += __ldg(part_p + (long long)(c + g) * E + e);
-            cnt += __ldg(part_c + (long long)(c + g) * E + e);
+    if (e < E) {
+        constexpr int B = 8;   // slots in flight (most groups have no more per thread)
+        for (int b0 = c0 + sub; b0 < c1; b0 += B * subs) {
+            float p[B];
+            int k[B];
+#pragma unroll
+            for (int j = 0; j < B; ++j) {
+                const int c = b0 + j * subs;
+                p[j] = c < c1 ? __ldg(part_p + (long long)(c + g) * E + e) : 0.f;
+                k[j] = c < c1 ? __ldg(part_c + (long long)(c + g) * E + e) : 0;
+            }
+#pragma unroll
+            for (int j = 0; j < B; ++j) { sum += p[j]; cnt += k[j]; }
         }
+    }
     s_p[tid] = sum;
     s_c[tid] = cnt;
     __syncthreads();
@@ -271,37 +280,33 @@ balance_reduce_kernel(const float* __restrict__ part_p, const int* __restrict__ 
     pdl_launch_dependents();
 }
 
-// One warp's slot gradients: (row of the warp, slot) pairs, 32 at a time, added to the rows in shared
-// memory in slot order.  An expert chosen twice by a row gets its terms one after the other.
-template <int LPR>
-__device__ __forceinline__ void bal_add_slots(float* rows, int n_rows, int E, int K, const int* __restrict__ ids,
-                                              const float* __restrict__ d_r, const float* __restrict__ d_l, int lane)
+// One (row of the warp, slot) pair per lane: its expert and gradients.
+struct BalSlot { int id; float gr, gl; };
+__device__ __forceinline__ BalSlot bal_slot(int i, int n, const int* __restrict__ ids, const float* __restrict__ d_r,
+                                            const float* __restrict__ d_l)
 {
-    for (int i0 = 0; i0 < n_rows * K; i0 += 32) {
-        const int i = i0 + lane;
-        int id = -1, row = 0;
-        float gr = 0.f, gl = 0.f;
-        if (i < n_rows * K) {
-            id = __ldg(ids + i);
-            gr = __ldg(d_r + i);
-            gl = __ldg(d_l + i);
-            row = i / K;
+    BalSlot s = {-1, 0.f, 0.f};
+    if (i < n) s = {__ldg(ids + i), __ldg(d_r + i), __ldg(d_l + i)};
+    return s;
+}
+// Adds the lanes' pairs to the rows in shared memory (row = pair / K), in slot order where a row has
+// chosen an expert twice.
+__device__ __forceinline__ void bal_add_slots(float* rows, const BalSlot& s, int row, int E, int lane)
+{
+    const bool on = s.id >= 0 && s.id < E;
+    const int key = on ? row * 256 + s.id : -1 - lane;
+    const unsigned same = __match_any_sync(0xffffffffu, key);
+    const bool twice = __any_sync(0xffffffffu, (same & (same - 1)) != 0);
+    float* p = rows + row * 2 * E + s.id;
+    if (!twice) {
+        if (on) { p[0] += s.gr; p[E] += s.gl; }
+    } else {
+        for (int k = 0; k < 32; ++k) {
+            if (lane == k && on) { p[0] += s.gr; p[E] += s.gl; }
+            __syncwarp();
         }
-        const bool on = id >= 0 && id < E;
-        const int key = on ? row * 256 + id : -1 - lane;
-        const unsigned same = __match_any_sync(0xffffffffu, key);
-        const bool twice = __any_sync(0xffffffffu, (same & (same - 1)) != 0);
-        float* p = rows + row * 2 * E + id;
-        if (!twice) {
-            if (on) { p[0] += gr; p[E] += gl; }
-        } else {
-            for (int k = 0; k < 32; ++k) {
-                if (lane == k && on) { p[0] += gr; p[E] += gl; }
-                __syncwarp();
-            }
-        }
-        __syncwarp();
     }
+    __syncwarp();
 }
 
 template <typename T, int LPR>
@@ -321,8 +326,10 @@ balance_grad_kernel(const T* __restrict__ logits, long long ldl, int n_tok, int 
     if (threadIdx.x == 0) s_act = 0;
     __syncthreads();
     int act = 0;
-    for (int i = threadIdx.x; i < G; i += kBalThreads) act += tokens[i] > 0;
-    if (act) atomicAdd(&s_act, act);
+    if (G > 1) {
+        for (int i = threadIdx.x; i < G; i += kBalThreads) act += tokens[i] > 0;
+        if (act) atomicAdd(&s_act, act);
+    }
     const long long t0 = (long long)blockIdx.x * run, t1 = min(t0 + run, (long long)n_tok);
     int g = cu ? bal_group(cu, n_seq, (int)t0) : 0;   // moves on with the lane's rows
     float v[kBalPer], f[kBalPer];
@@ -330,11 +337,11 @@ balance_grad_kernel(const T* __restrict__ logits, long long ldl, int n_tok, int 
     int g_of_f = -1;
     const int width = d_r ? 2 * E : E;
     float* rows = s_rows[warp];
-    __syncthreads();
-    act = s_act;
     long long t = t0 + warp * R + lane / LPR;
     bool here = t < t1;
     bal_load<T, LPR>(v, logits + t * ldl, r, E, here);
+    __syncthreads();
+    act = G > 1 ? s_act : 1;   // one group: the tokens that use it make it a non-empty one
     for (long long base = t0 + warp * R; base < t1; base += kBalWarps * R) {
         // the row's group, and f of that group where it is another than the last row's
         bool in = here && (!valid || valid[t]);
@@ -355,6 +362,11 @@ balance_grad_kernel(const T* __restrict__ logits, long long ldl, int n_tok, int 
         }
         float w[kBalPer];
         const bool cur = in && coef != 0.f;
+        // the first 32 slots of the warp's rows, on their way while the softmax runs
+        const int n_rows = (int)min((long long)R, t1 - base), n_slots = d_r ? n_rows * K : 0;
+        const int* ids = topk + base * K;
+        const float *gr = d_r + base * K, *gl = d_l + base * K;
+        const BalSlot first = bal_slot(lane, n_slots, ids, gr, gl);
         t += kBalWarps * R;
         here = t < t1;
         bal_load<T, LPR>(w, logits + t * ldl, r, E, here);
@@ -374,8 +386,11 @@ balance_grad_kernel(const T* __restrict__ logits, long long ldl, int n_tok, int 
             }
         }
         __syncwarp();
-        const int n_rows = (int)min((long long)R, t1 - base);
-        if (d_r) bal_add_slots<LPR>(rows, n_rows, E, K, topk + base * K, d_r + base * K, d_l + base * K, lane);
+        if (d_r) {
+            bal_add_slots(rows, first, lane / K, E, lane);
+            for (int i = 32; i < n_slots; i += 32)
+                bal_add_slots(rows, bal_slot(i + lane, n_slots, ids, gr, gl), (i + lane) / K, E, lane);
+        }
         // the rows are contiguous in memory
         float* o = out + base * width;
         const int total = n_rows * width;
