@@ -31,9 +31,9 @@
 // Measured on B200 (device time):
 //   dW 8192 x 1536 x 424, float32 G: 38 us, 280 TFLOP/s of dW's own operations, 0.84 PFLOP/s with the limbs;
 //     unsliced 92 us.  What bounds it is the loaders' work per step (converting and storing 40 KB per CTA):
-//     the MMAs alone take 20 of the 38 us.  1003 x 2048 x 128, bf16 G: 9.2 us (unsliced 12.2).
-//   dx 8192 x 2048 x 128, float32 G, bf16 W: 19.7 us, 67 MB written (floor 11 us at the copy rate); with A
-//     converted again for every n tile 34 us.  8192 x 1536 x 424 (A too long to stay): 56 us, bf16 G 24 us.
+//     the MMAs alone take 20 of the 38 us.  1003 x 2048 x 128, bf16 G: 8.7 us (unsliced 12.2).
+//   dx 8192 x 2048 x 128, float32 G, bf16 W: 19.5 us, 67 MB written (floor 11 us at the copy rate); with A
+//     converted again for every n tile 34 us.  8192 x 1536 x 424 (A too long to stay): 55 us, bf16 G 25 us.
 //   Error against 64 bits at 8192 x 1536 x 424: 1.1e-7; with the accumulator drained every 16 steps 2.1e-7,
 //     never 3.0e-6 (2.3e-6 of it towards zero), with one accumulator for all products 8.5e-7.
 #pragma once
