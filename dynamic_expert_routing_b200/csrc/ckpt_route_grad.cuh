@@ -146,7 +146,7 @@ ckpt_dot_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ scale,
     pdl_launch_dependents();
 }
 
-// Segments: a CTA per decision adds the tokens' dots (thread = slot and every 256/KP-th token, KP
+// Segments: a CTA per decision adds the tokens' dots in 64 bits (thread = slot and every 256/KP-th token, KP
 // the power of two that holds K; then the partials in thread order), and zeroes the gradients
 // of the segment's other tokens.
 __global__ void __launch_bounds__(kDotThreads)
@@ -154,12 +154,12 @@ ckpt_slot_grad_kernel(const float* __restrict__ s, int n_tok, int K, int kp, int
                       const float* __restrict__ gate, const float* __restrict__ mlogit, float reg,
                       float* __restrict__ d_r, float* __restrict__ d_l)
 {
-    __shared__ float s_part[kDotThreads];
+    __shared__ double s_part[kDotThreads];
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31;
     const long long t0 = (long long)blockIdx.x * S, t1 = min((long long)n_tok, t0 + S);
     const int k = tid & (kp - 1), step = kDotThreads / kp;
-    float run = 0.f;
+    double run = 0.0;
     if (k < K)
 #pragma unroll 4
         for (long long t = t0 + tid / kp; t < t1; t += step) run += __ldg(s + t * K + k);
@@ -168,12 +168,12 @@ ckpt_slot_grad_kernel(const float* __restrict__ s, int n_tok, int K, int kp, int
     __syncthreads();
     if (tid < 32) {
         const bool on = lane < K;
-        run = 0.f;
+        run = 0.0;
         if (on)
             for (int i = 0; i < step; ++i) run += s_part[i * kp + lane];
         const float g = on ? gate[t0 * K + lane] : 0.f, l = on ? mlogit[t0 * K + lane] : 0.f;
         float gr, gl;
-        slot_grads(on, run, g, l, (int)(t1 - t0), reg, gr, gl);
+        slot_grads(on, (float)run, g, l, (int)(t1 - t0), reg, gr, gl);
         if (on) { d_r[t0 * K + lane] = gr; d_l[t0 * K + lane] = gl; }
     }
     pdl_launch_dependents();
