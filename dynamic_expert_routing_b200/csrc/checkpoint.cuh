@@ -11,9 +11,11 @@
 // reads back as NaN.  k = 122, the largest, limits |q| to 63: 64 * 2^122 is past float32.
 // Rows of q are padded with zeros to a whole block, so that every row starts 32-byte aligned.
 //
-// Measured on B200 (save + load of 8192 x 4096, L2 warm): float16 31.5 us for 203 MB moved (6.4 TB/s), float32
-// 51.5 us for 337 MB (6.5 TB/s), at the measured copy rate; 20000 x 1413 bf16 (no row aligned on the way
-// out) 47.5 us for 171 MB; a warp per block with single values took 213 and 125 us.
+// Measured on B200 (save + load of 8192 x 4096, L2 warm): float16 29.0 us for 203 MB moved (7.0 TB/s: part of
+// q is still in L2 when it is read back), float32 51.5 us for 337 MB (6.5 TB/s), at the measured copy rate;
+// 20000 x 1413 bf16 (no row aligned on the way out) 45 us for 171 MB; a warp per block with single values took
+// 213 and 125 us.  With values widened to float32 one by one the integer pipe was busy for 80 % of the time
+// (save 19.9, load 18.1 us alone and cold); in pairs of 16 bits 15.6 and 15.2 us.
 #pragma once
 #include "common.cuh"
 
@@ -44,17 +46,20 @@ __device__ __forceinline__ float ckpt_step(int byte) { return __uint_as_float((u
 // leaves it in the low mantissa bits, in two's complement; x * inv_step is exact, so the fused
 // multiply-add is the one rounding.  (The conversion instruction would run at a quarter of the
 // rate.)  |x * inv_step| <= 127 by the choice of the scale.
-__device__ __forceinline__ uint32_t ckpt_quant4(const float* x, float inv_step, int byte)
+__device__ __forceinline__ uint32_t ckpt_quant4(const float* x, int byte)
 {
-    if (byte == kCkptNan) return 0u;
     constexpr float kRound = 12582912.f;
+    float v[4] = {x[0], x[1], x[2], x[3]};
+    if (byte >= 122 + kCkptBias) {   // hardly ever taken: the largest exponent, or a block of NaN
+        if (byte == kCkptNan) return 0u;
+        const float lim = 63.f * ckpt_step(byte);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = fminf(fmaxf(v[i], -lim), lim);
+    }
+    const float inv_step = ckpt_inv_step(byte);
     uint32_t r[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float v = x[i];
-        if (byte == 122 + kCkptBias) v = fminf(fmaxf(v, -63.f * ckpt_step(byte)), 63.f * ckpt_step(byte));
-        r[i] = __float_as_uint(fmaf(v, inv_step, kRound));
-    }
+    for (int i = 0; i < 4; ++i) r[i] = __float_as_uint(fmaf(v[i], inv_step, kRound));
     return __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410);
 }
 // The four integers of a word as floats: byte ^ 0x80 = q + 128 under the exponent of 2^23.
@@ -64,6 +69,87 @@ __device__ __forceinline__ void ckpt_unpack4(uint32_t w, float* f)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         f[i] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 + i)) - 8388736.f;
+}
+
+// q 2^k in pairs of bf16.  With u = q + 128 = 128 h + l, the byte l under 0x43 is the bf16 number 128 + l, and
+// the byte 128 (1 - h) under 0x43 is 128 or 256: their difference is q, exactly (8 significant bits), and so
+// is its product with 2^k.  (Going by float32 takes half as many instructions again.)  sel: 0x4140 for the
+// word's lower two bytes, 0x4342 for the upper two.
+__device__ __forceinline__ uint32_t ckpt_pair(uint32_t w, uint32_t sel, __nv_bfloat162 step)
+{
+    const uint32_t a = __byte_perm(w & 0x7f7f7f7fu, 0x43u, sel), c = __byte_perm(w & 0x80808080u, 0x43u, sel);
+    const __nv_bfloat162 q = __hsub2(reinterpret_cast<const __nv_bfloat162&>(a), reinterpret_cast<const __nv_bfloat162&>(c));
+    const __nv_bfloat162 v = __hmul2(q, step);
+    return reinterpret_cast<const uint32_t&>(v);
+}
+__device__ __forceinline__ __nv_bfloat162 ckpt_step_pair(int byte)
+{
+    const uint32_t k = (uint32_t)byte << 7, k2 = k | k << 16;
+    return reinterpret_cast<const __nv_bfloat162&>(k2);
+}
+// The same in float16 for scale bytes in [103, 136], where 2^k is a float16 and no product passes its range:
+// q + 128 under 0x64 is 1024 + (q + 128).  Products below 2^-14 round like any float16.
+__device__ __forceinline__ uint32_t ckpt_pair(uint32_t w, uint32_t sel, __half2 step)
+{
+    const uint32_t a = __byte_perm(w ^ 0x80808080u, 0x64u, sel);
+    const __half2 v = __hmul2(__hsub2(reinterpret_cast<const __half2&>(a), __float2half2_rn(1152.f)), step);
+    return reinterpret_cast<const uint32_t&>(v);
+}
+
+// ---------------------------------------------------------------- one 16-byte vector of the wide type
+// The arithmetic below is what bounded the copies before it was done in pairs (the integer pipe at 80 %).
+// A key of the largest magnitude in a vector, ordered like it (NaN on top), ...
+__device__ __forceinline__ uint32_t ckpt_amax(const uint4& v, float)
+{
+    float m = 0.f;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(__uint_as_float(w[i]))));
+    return __float_as_uint(m);
+}
+__device__ __forceinline__ uint32_t ckpt_amax16(const uint4& v)
+{
+    const uint32_t k = 0x7fff7fffu;
+    const uint32_t m = __vmaxu2(__vmaxu2(v.x & k, v.y & k), __vmaxu2(v.z & k, v.w & k));
+    return max(m & 0xffffu, m >> 16);
+}
+__device__ __forceinline__ uint32_t ckpt_amax(const uint4& v, __half) { return ckpt_amax16(v); }
+__device__ __forceinline__ uint32_t ckpt_amax(const uint4& v, __nv_bfloat16) { return ckpt_amax16(v); }
+// ... and its float32 bits.
+__device__ __forceinline__ uint32_t ckpt_key_bits(uint32_t key, float) { return key; }
+__device__ __forceinline__ uint32_t ckpt_key_bits(uint32_t key, __nv_bfloat16) { return key << 16; }
+__device__ __forceinline__ uint32_t ckpt_key_bits(uint32_t key, __half)
+{
+    return __float_as_uint(__half2float(__ushort_as_half((unsigned short)key)));
+}
+
+// The vector's V quantised bytes (float32: the lower word).
+template <typename T>
+__device__ __forceinline__ uint2 ckpt_quant(const uint4& raw, int byte)
+{
+    constexpr int V = Vec<T>::N;
+    float v[8];
+    Vec<T>::widen(raw, v);
+    return make_uint2(ckpt_quant4(v, byte), V == 8 ? ckpt_quant4(v + V - 4, byte) : 0u);
+}
+// float16: 1.5 * 2^10 rounds to an integer as 1.5 * 2^23 does in float32, where 2^-k is a float16.
+template <>
+__device__ __forceinline__ uint2 ckpt_quant<__half>(const uint4& raw, int byte)
+{
+    if (byte < kCkptBias - 15 || byte > kCkptBias + 10) {
+        float v[8];
+        Vec<__half>::widen(raw, v);
+        return make_uint2(ckpt_quant4(v, byte), ckpt_quant4(v + 4, byte));
+    }
+    const __half2 inv = __float2half2_rn(ckpt_inv_step(byte)), round = __float2half2_rn(1536.f);
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 h = __hfma2(reinterpret_cast<const __half2&>(w[i]), inv, round);
+        r[i] = reinterpret_cast<const uint32_t&>(h);
+    }
+    return make_uint2(__byte_perm(r[0], r[1], 0x6420), __byte_perm(r[2], r[3], 0x6420));
 }
 
 // Position of a unit u of a [rows][per_row] grid, advanced by a fixed step without dividing.
@@ -145,21 +231,14 @@ ckpt_save_kernel(const T* __restrict__ x, long long ldx, long long rows, int D, 
 #pragma unroll
     for (int i = 0; i < U; ++i) {
         const long long u = u0 + i * kCkptThreads;
-        float v[V];
-        Vec<T>::widen(raw[i].u, v);
-        uint32_t a = 0u;
-#pragma unroll
-        for (int j = 0; j < V; ++j) a = max(a, __float_as_uint(v[j]) & 0x7fffffffu);
+        uint32_t a = ckpt_amax(raw[i].u, T());
 #pragma unroll
         for (int o = 1; o < L; o <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-        const int byte = ckpt_scale_byte(a);
-        const float inv = ckpt_inv_step(byte);
+        const int byte = ckpt_scale_byte(ckpt_key_bits(a, T()));
+        const uint2 b = ckpt_quant<T>(raw[i].u, byte);
         if (u < n) {
-            if (V == 8)
-                *reinterpret_cast<uint2*>(q + u * V) =
-                    make_uint2(ckpt_quant4(v, inv, byte), ckpt_quant4(v + V - 4, inv, byte));
-            else
-                *reinterpret_cast<uint32_t*>(q + u * V) = ckpt_quant4(v, inv, byte);
+            if (V == 8) *reinterpret_cast<uint2*>(q + u * V) = b;
+            else *reinterpret_cast<uint32_t*>(q + u * V) = b.x;
             if ((threadIdx.x & (L - 1)) == 0) scale[u / L] = (uint8_t)byte;
         }
     }
@@ -183,6 +262,43 @@ __device__ __forceinline__ uint4 ckpt_pack(const float* f)
 #pragma unroll
     for (int j = 0; j < V; ++j) o.t[j] = ckpt_value<T>(f[j]);
     return o.u;
+}
+
+// V values of one block from their bytes.
+template <typename T>
+__device__ __forceinline__ uint4 ckpt_values(const uint2& q, int byte)
+{
+    constexpr int V = Vec<T>::N;
+    float f[8];
+    ckpt_unpack4(q.x, f);
+    if (V == 8) ckpt_unpack4(q.y, f + 4);
+    const float step = ckpt_step(byte);
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] *= step;
+    return ckpt_pack<T>(f);
+}
+template <typename S>
+__device__ __forceinline__ uint4 ckpt_pairs(const uint2& q, S step)
+{
+    return make_uint4(ckpt_pair(q.x, 0x4140, step), ckpt_pair(q.x, 0x4342, step), ckpt_pair(q.y, 0x4140, step),
+                      ckpt_pair(q.y, 0x4342, step));
+}
+template <>
+__device__ __forceinline__ uint4 ckpt_values<__nv_bfloat16>(const uint2& q, int byte)
+{
+    return ckpt_pairs(q, ckpt_step_pair(byte));
+}
+template <>
+__device__ __forceinline__ uint4 ckpt_values<__half>(const uint2& q, int byte)
+{
+    if (byte >= kCkptBias - 24 && byte <= kCkptBias + 9) return ckpt_pairs(q, __float2half2_rn(ckpt_step(byte)));
+    float f[8];
+    ckpt_unpack4(q.x, f);
+    ckpt_unpack4(q.y, f + 4);
+    const float step = ckpt_step(byte);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] *= step;
+    return ckpt_pack<__half>(f);
 }
 
 // y [rows][D] contiguous and 16-byte aligned.  FLAT: D a multiple of 32; ROWS: of V.
@@ -213,16 +329,11 @@ ckpt_load_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ scale
 #pragma unroll
     for (int i = 0; i < kCkptUnroll; ++i) {
         const long long u = u0 + i * kCkptThreads;
-        float f[8];
-        ckpt_unpack4(raw[i].x, f);
-        if (V == 8) ckpt_unpack4(raw[i].y, f + 4);
-        const float step = ckpt_step(byte[i]);
-#pragma unroll
-        for (int j = 0; j < V; ++j) f[j] *= step;
+        const uint4 v = ckpt_values<T>(raw[i], byte[i]);
         if (ROWS == CKPT_FLAT) {
-            if (u < n) *reinterpret_cast<uint4*>(y + u * V) = ckpt_pack<T>(f);
+            if (u < n) *reinterpret_cast<uint4*>(y + u * V) = v;
         } else {
-            if (u < n && pos.at * V < D) *reinterpret_cast<uint4*>(y + pos.row * D + pos.at * V) = ckpt_pack<T>(f);
+            if (u < n && pos.at * V < D) *reinterpret_cast<uint4*>(y + pos.row * D + pos.at * V) = v;
             pos.advance();
         }
     }

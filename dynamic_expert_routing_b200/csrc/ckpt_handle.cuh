@@ -51,7 +51,7 @@ ckpt_experts_kernel(const TY* __restrict__ yperm, int splits, long long stride, 
         for (int o = 1; o < L; o <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
         const int byte = ckpt_scale_byte(a);
         if (u < n) {
-            *reinterpret_cast<uint32_t*>(q + u * 4) = ckpt_quant4(f, ckpt_inv_step(byte), byte);
+            *reinterpret_cast<uint32_t*>(q + u * 4) = ckpt_quant4(f, byte);
             if ((threadIdx.x & (L - 1)) == 0) scale[u / L] = (uint8_t)byte;
         }
     }

@@ -214,22 +214,9 @@ __device__ __forceinline__ uint32_t pack_hi(uint32_t lo, uint32_t hi) { return _
 
 // bf16 limbs of the eight values, most significant first.
 __device__ __forceinline__ void raw_limbs(const Raw<SRC_BF16>& r, uint4* o) { o[0] = r.a; }
-// q 2^k in pairs of bf16.  With u = q + 128 = 128 h + l, the byte l under 0x43 is the bf16 number 128 + l, and
-// the byte 128 (1 - h) under 0x43 is 128 or 256: their difference is q, exactly (8 significant bits), and so
-// is its product with 2^k.  (Going by float32 takes half as many instructions again.)
-__device__ __forceinline__ uint32_t ckpt_pair(uint32_t w, uint32_t sel, __nv_bfloat162 step)
-{
-    const uint32_t a = __byte_perm(w & 0x7f7f7f7fu, 0x43u, sel), c = __byte_perm(w & 0x80808080u, 0x43u, sel);
-    const __nv_bfloat162 q = __hsub2(reinterpret_cast<const __nv_bfloat162&>(a), reinterpret_cast<const __nv_bfloat162&>(c));
-    const __nv_bfloat162 v = __hmul2(q, step);
-    return reinterpret_cast<const uint32_t&>(v);
-}
 __device__ __forceinline__ void raw_limbs(const Raw<SRC_CKPT>& r, uint4* o)
 {
-    const uint32_t k = (uint32_t)r.byte << 7, k2 = k | k << 16;
-    const __nv_bfloat162 step = reinterpret_cast<const __nv_bfloat162&>(k2);
-    o[0] = make_uint4(ckpt_pair(r.w.x, 0x4140, step), ckpt_pair(r.w.x, 0x4342, step), ckpt_pair(r.w.y, 0x4140, step),
-                      ckpt_pair(r.w.y, 0x4342, step));
+    o[0] = ckpt_pairs(r.w, ckpt_step_pair(r.byte));
 }
 __device__ __forceinline__ void raw_limbs(const Raw<SRC_F32>& r, uint4* o)
 {

@@ -227,6 +227,28 @@ def test_checkpoint_extreme_values():
     np.testing.assert_array_equal(half[12], np.clip(want[12], -65504, 65504))
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("order", ["neighbours", "mixed"])
+def test_checkpoint_every_16_bit_value(dtype, order):
+    """All 65536 patterns, in blocks of neighbouring values and in mixed ones (most of those hold a NaN for
+    float16, so the values alone are mixed); every decoded value in each type, float16's rounding included."""
+    b = beam()
+    v = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(dtype)
+    if order == "mixed":
+        v = v[torch.isfinite(v)]
+        v = v[torch.from_numpy(np.random.default_rng(5).permutation(v.numel()))]
+    v = v[:v.numel() // 256 * 256].reshape(-1, 256)
+    c = b.checkpoint_save(v.cuda())
+    q, byte = ref.encode(np64(v))
+    np.testing.assert_array_equal(c["scale"].cpu().numpy(), byte)
+    np.testing.assert_array_equal(c["q"].cpu().numpy(), q)
+    want = ref.decode(q, byte, 256)
+    for out in (torch.float32, torch.bfloat16):
+        np.testing.assert_array_equal(np64(b.checkpoint_load(c, out)), want)
+    half = np.clip(want, -65504, 65504).astype(np.float16).astype(np.float64)
+    np.testing.assert_array_equal(np64(b.checkpoint_load(c, torch.float16)), half)
+
+
 def test_checkpoint_past_32_bit_offsets():
     b = beam()
     N, D = (1 << 20) + 3, 4128
