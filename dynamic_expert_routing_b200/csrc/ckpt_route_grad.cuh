@@ -6,12 +6,14 @@
 //   d_l_k = dmh_k sigmoid(l_k)(1 - sigmoid(l_k));  d_r_k = g_k (dg_k - sum_j g_j dg_j)
 // The decision's gradients go to its first token; the others of a segment get 0.
 // HBM-bound: one byte per expert-output value and dy once; at K = 16 the unpacking (a byte permute
-// and an add per value) and the multiply-adds are within a factor of two of the memory time, so
-// nothing else may enter the inner loop.
+// and half an add per value) and the multiply-adds (half an instruction) are within a factor of two of the
+// memory time, so nothing else may enter the inner loop.
 //
-// Measured on B200: 8192 tokens x 16 slots x 1536, float32 dy: 49 us, 261 MB, 5.3 TB/s (81 % of the measured
-// copy rate; 8-byte loads of q for all slots at once, 141 registers: 95 us; four slots in flight instead of
-// eight, at any occupancy: 54-65 us).  33 x 2 x 4096: 2.1 us with eight warps per token, 5.7 with one.
+// Measured on B200: 8192 tokens x 16 slots x 1536, float32 dy: 47.3 us, 261 MB, 5.5 TB/s (84 % of the measured
+// copy rate; the loads without the arithmetic take 44).  8-byte loads of q for all slots at once, 141 registers: 95 us;
+// four slots in flight instead of eight, at any occupancy: 54-65 us; q and dy through a shared-memory ring of
+// asynchronous copies, 90 KB per SM in flight: 57 us; two warps per token, eight slots each: 50 us.
+// 33 x 2 x 4096: 2.25 us with eight warps per token, 5.7 with one.
 #pragma once
 #include "checkpoint.cuh"
 
@@ -65,10 +67,56 @@ __device__ __forceinline__ void load_dy16(const T* __restrict__ row, int c, int 
     }
 }
 
+// Two floats in a register pair: the f32x2 instructions add, or multiply and add, both in one issue slot, each
+// rounded by itself.
+__device__ __forceinline__ unsigned long long f32_pair(float lo, float hi)
+{
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+// a += the word's four values times f: the even columns in the lower half, the odd ones in the upper.
+__device__ __forceinline__ void dot4_pairs(uint32_t w, const float* f, unsigned long long& a)
+{
+    const unsigned long long off = f32_pair(-8388736.f, -8388736.f);   // ckpt_unpack4's
+    w ^= 0x80808080u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        unsigned long long v = f32_pair(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 + 2 * i)),
+                                        __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7441 + 2 * i)));
+        asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(v), "l"(off));
+        asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(v), "l"(f32_pair(f[2 * i], f[2 * i + 1])));
+    }
+}
+
+// The scale bytes of a strip (512 columns, 16 blocks from block b0 on) of up to eight slots, four blocks of a slot
+// per lane: one load where rows of scales are 4-byte aligned.  (A byte per lane and slot instead: 4 us of 49, for
+// 8192 x 16 x 1536.)
+__device__ __forceinline__ uint32_t load_scales(const uint8_t* __restrict__ st, int nb, int k0, int slots, int b0, int lane,
+                                                bool words)
+{
+    const int b = b0 + 4 * (lane & 3);
+    const uint8_t* p = st + (long long)(k0 + min(lane >> 2, slots - 1)) * nb + b;
+    if (b >= nb) return 0u;
+    if (words) return __ldg(reinterpret_cast<const uint32_t*>(p));
+    uint32_t r = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (b + i < nb) r |= (uint32_t)__ldg(p + i) << (8 * i);
+    return r;
+}
+// 2^k of the lane's block (lane / 2) of slot k.
+__device__ __forceinline__ float strip_step(uint32_t scales, int k, int lane)
+{
+    const uint32_t w = __shfl_sync(0xffffffffu, scales, 4 * k + (lane >> 3));
+    return __uint_as_float(__byte_perm(w, 0u, ((lane >> 1 & 3) << 12) | 0x0444) >> 1);
+}
+
 // KM: the smallest of 2, 4, 8, 16, 32 that holds K.  WPT warps share a token, each taking every
 // WPT-th strip of its columns for all K slots (dy is read once per token); their sums are added in
-// warp order.  With one-token decisions (grads) the slot gradients follow in the same kernel.
-template <typename T, int KM>
+// warp order.  U strips are loaded together: two where K <= 2 and a warp has them (4096 x 2 x 4096 20.0 us, one
+// by one 22.1).  With one-token decisions (grads) the slot gradients follow in the same kernel.
+template <typename T, int KM, int U>
 __global__ void __launch_bounds__(kDotThreads, KM <= 16 ? 2 : 1)
 ckpt_dot_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ scale, int n_tok, int K,
                 int D, int nb, const T* __restrict__ dy, long long lddy, int vec, int wpt,
@@ -89,42 +137,44 @@ ckpt_dot_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ scale,
 #pragma unroll
     for (int k = 0; k < KM; ++k) acc[k] = 0.f;
     if (live) {
-        constexpr int B = KM < 8 ? KM : 8;   // slots whose loads are in flight together
+        constexpr int B = KM < 8 ? KM : 8;   // slots whose loads are in flight together, in U strips
         const T* dyr = dy + t * lddy;
         const int Dp = nb * kCkptBlock;
         const int8_t* qt = q + t * K * Dp;
         const uint8_t* st = scale + t * K * nb;
+        const bool words = (nb & 3) == 0 && (reinterpret_cast<uintptr_t>(scale) & 3) == 0;
 #pragma unroll 1
-        for (int c = (sub * 32 + lane) * 16; c < Dp; c += wpt * kDotCols) {
-            float f[16];
-            load_dy16(dyr, c, D, vec, f);
-            const int8_t* qc = qt + c;
-            const uint8_t* sc = st + c / kCkptBlock;
+        for (int c0 = sub * kDotCols; c0 < Dp; c0 += U * wpt * kDotCols) {
+            float f[U][16];
+#pragma unroll
+            for (int u = 0; u < U; ++u) load_dy16(dyr, c0 + u * wpt * kDotCols + lane * 16, D, vec, f[u]);
 #pragma unroll
             for (int k0 = 0; k0 < KM; k0 += B) {
                 if (k0 >= K) break;
-                uint4 w[B];
-                int byte[B];
+                uint4 w[U][B];
+                uint32_t scales[U];
 #pragma unroll
-                for (int k = 0; k < B; ++k) {
-                    // slots past K repeat the last one: no branch, and their sums are dropped
-                    const int ks = min(k0 + k, K - 1);
-                    w[k] = __ldcs(reinterpret_cast<const uint4*>(qc + ks * Dp));
-                    byte[k] = __ldg(sc + ks * nb);
+                for (int u = 0; u < U; ++u) {
+                    const int cu = c0 + u * wpt * kDotCols, c = min(cu + lane * 16, Dp - 16);
+                    scales[u] = load_scales(st, nb, k0, min(B, K - k0), cu / kCkptBlock, lane, words);
+#pragma unroll
+                    for (int k = 0; k < B; ++k)
+                        // slots past K repeat the last one: no branch, and their sums are dropped
+                        w[u][k] = __ldcs(reinterpret_cast<const uint4*>(qt + c + min(k0 + k, K - 1) * Dp));
                 }
 #pragma unroll
-                for (int k = 0; k < B; ++k) {
-                    const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-                    float a0 = 0.f, a1 = 0.f;
+                for (int u = 0; u < U; ++u)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float v[4];
-                        ckpt_unpack4(u[j], v);
-                        a0 = fmaf(v[0], f[4 * j], a0); a1 = fmaf(v[1], f[4 * j + 1], a1);
-                        a0 = fmaf(v[2], f[4 * j + 2], a0); a1 = fmaf(v[3], f[4 * j + 3], a1);
+                    for (int k = 0; k < B; ++k) {
+                        const uint32_t x[4] = {w[u][k].x, w[u][k].y, w[u][k].z, w[u][k].w};
+                        unsigned long long a = 0ull;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) dot4_pairs(x[j], f[u] + 4 * j, a);
+                        float a0, a1;
+                        asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
+                        // lanes past the row: dy and the scale are 0
+                        acc[k0 + k] = fmaf(a0 + a1, strip_step(scales[u], k, lane), acc[k0 + k]);
                     }
-                    acc[k0 + k] = fmaf(a0 + a1, ckpt_step(byte[k]), acc[k0 + k]);
-                }
             }
         }
     }

@@ -306,11 +306,12 @@ beam_status_t beam_checkpoint_route_grad(const int8_t* q, const uint8_t* scale, 
                                K, d, nb, (const TY*)dy, (long long)ld_dy, (int)(!misaligned(dy, 16) && ld_dy % Vec<TY>::N == 0),
                                wpt, gate, mask_logit, reg, (int)grads, dghat, d_gate_logit, d_mask_logit);
         };
-        if (K <= 2) return go(ckpt_dot_kernel<TY, 2>);
-        if (K <= 4) return go(ckpt_dot_kernel<TY, 4>);
-        if (K <= 8) return go(ckpt_dot_kernel<TY, 8>);
-        if (K <= 16) return go(ckpt_dot_kernel<TY, 16>);
-        return go(ckpt_dot_kernel<TY, 32>);
+        if (K <= 2 && d > wpt * kDotCols) return go(ckpt_dot_kernel<TY, 2, 2>);
+        if (K <= 2) return go(ckpt_dot_kernel<TY, 2, 1>);
+        if (K <= 4) return go(ckpt_dot_kernel<TY, 4, 1>);
+        if (K <= 8) return go(ckpt_dot_kernel<TY, 8, 1>);
+        if (K <= 16) return go(ckpt_dot_kernel<TY, 16, 1>);
+        return go(ckpt_dot_kernel<TY, 32, 1>);
     }));
     if (!grads) {
         int kp = 1;

@@ -269,7 +269,8 @@ def test_checkpoint_past_32_bit_offsets():
 # ------------------------------------------------------------------------------ slot gradients
 @pytest.mark.parametrize("T,K,D,seg", [(1, 1, 32, 0), (1, 2, 4096, 0), (33, 2, 4096, 0), (7, 32, 100, 0), (50, 6, 2048, 16),
                                        (37, 16, 1536, 16), (5, 3, 1, 0), (300, 5, 257, 7), (9, 4, 8191, 65536),
-                                       (700, 8, 64, 256), (2000, 16, 96, 0)])
+                                       (700, 8, 64, 256), (2000, 16, 96, 0), (2500, 2, 1500, 0),
+                                       (2500, 1, 1025, 0), (2400, 2, 2560, 0)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_route_grad_from_checkpoint(T, K, D, seg, dtype):
     b = beam()
@@ -300,6 +301,26 @@ def test_route_grad_from_checkpoint(T, K, D, seg, dtype):
             (K + 16) * U * (seg_mag + seg_mag.sum(1, keepdims=True)) + 1e-30).all()
     off = np.arange(T) % S != 0
     assert not np64(out["d_gate_logit"])[off].any() and not np64(out["d_mask_logit"])[off].any()
+
+
+@pytest.mark.parametrize("T,K,D", [(3, 20, 1537), (2400, 2, 1100), (2, 2, 4096), (3, 8, 2048)])
+def test_route_grad_lost_blocks_stay_in_their_slot(T, K, D):
+    """A non-finite value loses its block: its own slot's gradients are NaN, the token's other slots and
+    the other tokens' get the numbers that they get without it."""
+    b = beam()
+    y = rnd(1, T * K, D)
+    gate, ml, dy = torch.softmax(rnd(2, T, K), 1), rnd(3, T, K).abs(), rnd(4, T, D)
+    def run(v):
+        out = b.checkpoint_route_grad(b.checkpoint_save(v.cuda()), gate.cuda(), ml.cuda(), dy.cuda())
+        return np64(out["dghat"])
+    clean = run(y)
+    for t, k, c in [(0, 0, 0), (T - 1, K - 1, D - 1), (T // 2, K // 2, D // 2), (1, K - 1, 512)]:
+        v = y.clone()
+        v[t * K + k, c] = float("inf")
+        got = run(v)
+        assert np.isnan(got[t, k])
+        got[t, k] = clean[t, k]
+        np.testing.assert_array_equal(got, clean)
 
 
 # ------------------------------------------------------------------------------ linear backward
