@@ -184,7 +184,7 @@ Tensor balance_loss_backward(const Tensor& logits, const Tensor& topk, const py:
         gl = array("d_mask_logit", *d_mask, at::kFloat, {m.rows, g.K}, logits);
     }
     const On on(logits);
-    Tensor out = on.empty({m.rows, gr ? 2 * m.cols : m.cols}, at::kFloat);
+    Tensor out = on.empty({m.rows, d_gate ? 2 * m.cols : m.cols}, at::kFloat);
     done(api.balance_backward(m.p, m.type, (int32_t)m.rows, (int32_t)m.cols, m.ld, g.ids, (int32_t)g.K, g.valid, g.cu,
                               (int32_t)g.n, static_cast<int32_t*>(counts), static_cast<int32_t*>(tokens), (float)scale,
                               static_cast<float*>(gr), static_cast<float*>(gl), out.data_ptr<float>(), on.stream));

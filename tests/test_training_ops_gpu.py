@@ -184,6 +184,10 @@ def test_empty_batches():
     assert b.router_input_grad(torch.zeros((0, 5), device="cuda"), torch.zeros((7, 5), device="cuda")).shape == (0, 7)
     e = torch.zeros((0, 3), device="cuda")
     assert b.checkpoint_route_grad(c, e, e, z)["dghat"].shape == (0, 3)
+    slots = torch.zeros((0, 2), device="cuda")
+    g = b.balance_loss_backward(z, ids, out, d_gate_logit=slots, d_mask_logit=slots)
+    assert g.shape == (0, 16)
+    assert b.router_weight_grad(c, g, parts=2).shape == (2, 8, 8)
 
 
 # ------------------------------------------------------------------------------ checkpoints
