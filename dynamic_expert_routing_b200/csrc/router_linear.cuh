@@ -13,7 +13,7 @@
 // its own (the small ones share another), and every kChain steps of 64 the accumulators are
 // drained into float32 sums in registers, rounded to nearest.
 //
-// One kernel computes out[m][n] = sum_k A(m, k) B(n, k) on 256 x 128 tiles, 64 of k per step:
+// One kernel computes out[m][n] = sum_k A(m, k) B(n, k) on 256 x 128 tiles (256 x 64 for dW of up to 64 logits), 64 of k per step:
 //   dW: m = d, n = c, k = t: A and B lie in memory with m, n contiguous ("MN-major");
 //   dx: m = t, n = d, k = c: k contiguous ("K-major"; MN-major for a repacked W [C][D]).
 // Two CTAs share a tile (cta_group::2): each converts its 128 rows of A and half of B, so an operand
@@ -44,9 +44,9 @@
 namespace beam {
 namespace lin {
 
-constexpr int BM = 256, BN = 128, BK = 64;    // the tile of a CTA pair
-constexpr int kRowsA = BM / 2, kRowsB = BN / 2;   // a CTA's share of the operands
-constexpr int kLimbA = kRowsA * BK * 2, kLimbB = kRowsB * BK * 2;   // bytes of one limb of a share
+constexpr int BM = 256, kBN = 128, BK = 64;   // the tile of a CTA pair (BN = 64 where n is short, see NARROW)
+constexpr int kRowsA = BM / 2;                // a CTA's share of A, half a tile like that of B
+constexpr int kLimbA = kRowsA * BK * 2, kLimbB = kBN / 2 * BK * 2;   // bytes of one limb of a share
 constexpr int kChain = 4;                     // steps added in the tensor cores' accumulator
 // Warpgroups of 4 warps: 4 that load and convert, one whose first warp issues the MMAs, 2 that drain.
 // The kernel is launched with 72 registers a thread (7 x 128 x 72 of the SM's 65536); the
@@ -259,8 +259,12 @@ template <int SRC, bool MN, int ROWS> struct Cursor {
     static constexpr int ES = SRC == SRC_CKPT ? 1 : (SRC == SRC_F32 ? 4 : 2);
     static constexpr int kChunks = MN ? ROWS / 8 : 8;
     static constexpr int kRows = 32 * kLoadWarps / kChunks;        // rows of a block between pieces
-    static constexpr int kPieces = (MN ? BK : ROWS) / kRows;
+    static constexpr int kSpan = MN ? BK : ROWS;                   // rows of a block
+    static constexpr int kPieces = kSpan > kRows ? kSpan / kRows : 1;
     static_assert(kPieces <= 2, "one distance between pieces");
+    // The threads that have a piece: all, or the first warps where the share is small.
+    static __device__ __forceinline__ bool busy(int tid) { return kSpan >= kRows || tid < kSpan * kChunks; }
+    static_assert(kSpan * kChunks % 32 == 0, "whole warps");
     const char* p;           // piece 0 of the current step
     const uint8_t* sc;
     long long next;          // bytes from piece 0 to piece 1
@@ -326,10 +330,14 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t saddr)
     return tc::sw128_desc(saddr) - ((uint64_t)1 << 16) + ((uint64_t)((BK * 128) >> 4) << 16);
 }
 
-template <int SA, bool MNA, int SB, bool MNB, bool VEC, bool RES>
+// NARROW: tiles of 64 columns, for n <= 64 (MN-major B only: a share's 32 columns take the lower half of each
+// 128-byte row).  dW 4096 x 4096 x 16 14.5 us, with 128 columns 16.3.
+template <int SA, bool MNA, int SB, bool MNB, bool VEC, bool RES, bool NARROW>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 lin_gemm_kernel(const __grid_constant__ Params p)
 {
+    constexpr int BN = NARROW ? kBN / 2 : kBN, kRowsB = BN / 2;
+    static_assert(!NARROW || (MNB && !RES), "not built");
     constexpr int LA = limbs(SA), LB = limbs(SB), ST = RES ? res_stages<SB>() : stages<SA, SB>(), ACC = accs<SA, SB>();
     constexpr int kStage = RES ? LB * kLimbB : stage_bytes<SA, SB>();   // bytes of a ring stage
     constexpr int kTmemCols = 512;   // 2 sets of ACC accumulators of BN columns, at the same place in both CTAs
@@ -386,6 +394,8 @@ lin_gemm_kernel(const __grid_constant__ Params p)
         using CA = Cursor<SA, MNA, kRowsA>;
         using CB = Cursor<SB, MNB, kRowsB>;
         constexpr int PA = CA::kPieces, PB = CB::kPieces;
+        static_assert(CA::kSpan >= CA::kRows, "every thread has pieces of A");
+        const bool b_on = CB::busy(tid);
         const uint32_t oa = CA::offset(tid), ob = CB::offset(tid) + ring + bpart;
         CA ca;
         CB cb;
@@ -420,8 +430,9 @@ lin_gemm_kernel(const __grid_constant__ Params p)
             if (!RES)
 #pragma unroll
                 for (int i = 0; i < PA; ++i) ca.template load<VEC>(r.a[RES ? 0 : i], i, p.K);
+            if (b_on)
 #pragma unroll
-            for (int i = 0; i < PB; ++i) cb.template load<VEC>(r.b[i], i, p.K);
+                for (int i = 0; i < PB; ++i) cb.template load<VEC>(r.b[i], i, p.K);
         };
         int s = 0;
         uint32_t ph = 0;
@@ -438,6 +449,7 @@ lin_gemm_kernel(const __grid_constant__ Params p)
                     if (ALL) ca.load_all(v, i);
                     else ca.template load<VEC>(v, i, p.K);
                 }
+            if (b_on)
 #pragma unroll
             for (int i = 0; i < PB; ++i) {
                 piece_store<SB, kLimbB>(r.b[i], sm + ob + i * (CB::kRows * 128));
@@ -564,7 +576,7 @@ lin_gemm_kernel(const __grid_constant__ Params p)
         // ------------------------------------------------ epilogue: TMEM -> float32 sums -> global
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
         const int lb = 32 * (warp & 3);                    // TMEM lanes this warp may access
-        const int half = (warp - kEpiWarp0) / 4;           // which 64 columns
+        const int half = (warp - kEpiWarp0) / 4;           // which half of the columns
         int buf = 0;
         uint32_t bph = 0;
         bool ok = true;
@@ -579,7 +591,7 @@ lin_gemm_kernel(const __grid_constant__ Params p)
                 if (ok) ok = tc::mbar_wait(tfull_bar(buf), bph, abort_flag);
                 if (!ok) break;
                 tc::tc_fence_after();
-                const uint32_t d0 = tmem_base + ((uint32_t)lb << 16) + (uint32_t)(buf * ACC * BN + 64 * half);
+                const uint32_t d0 = tmem_base + ((uint32_t)lb << 16) + (uint32_t)(buf * ACC * BN + BN / 2 * half);
 #pragma unroll
                 for (int a = ACC - 1; a >= 0; --a)     // the small products first
 #pragma unroll
@@ -602,8 +614,8 @@ lin_gemm_kernel(const __grid_constant__ Params p)
             const int m0 = t.m0 + rank * kRowsA + lb, rows = min(32, p.M - m0);
             float* out = p.out + t.slice * p.slice;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int c0 = nt * BN + 64 * half + 32 * h;
+            for (int h = 0; h < BN / 64; ++h) {
+                const int c0 = nt * BN + BN / 2 * half + 32 * h;
                 __syncwarp();
 #pragma unroll
                 for (int j = 0; j < 32; j += 4)

@@ -348,12 +348,12 @@ static void plan_slices(lin::Params& p, int pairs)
     p.units = (int)(tiles * ceil_div(p.k_steps, p.split_steps));
 }
 
-static lin::Params lin_params(int M, int N, int K)
+static lin::Params lin_params(int M, int N, int K, bool narrow = false)
 {
     lin::Params p = {};
     p.M = M; p.N = N; p.K = K;
     p.m_tiles = (int)ceil_div(M, lin::BM);
-    p.n_tiles = (int)ceil_div(N, lin::BN);
+    p.n_tiles = (int)ceil_div(N, narrow ? lin::kBN / 2 : lin::kBN);
     p.k_steps = (int)ceil_div(K, lin::BK);
     p.split_steps = p.k_steps;
     p.units = p.m_tiles * p.n_tiles;
@@ -384,10 +384,10 @@ static void plan_ranges(lin::Params& p, int pairs)
     }
 }
 
-template <int SA, bool MNA, int SB, bool MNB, bool VEC, bool RES>
+template <int SA, bool MNA, int SB, bool MNB, bool VEC, bool RES, bool NARROW = false>
 static cudaError_t launch_lin_as(const lin::Params& p, int pairs, cudaStream_t st)
 {
-    auto kernel = lin::lin_gemm_kernel<SA, MNA, SB, MNB, VEC, RES>;
+    auto kernel = lin::lin_gemm_kernel<SA, MNA, SB, MNB, VEC, RES, NARROW>;
     const int smem = RES ? lin::res_bytes<SA, SB>(p.k_steps) : lin::smem_bytes<SA, SB>();
     static std::atomic<unsigned long long> ready;   // devices whose attribute is set
     int dev = 0;
@@ -415,19 +415,25 @@ static cudaError_t launch_rows(lin::Params p, int pairs, cudaStream_t st)
                : launch_lin_as<SA, MNA, SB, MNB, false, false>(p, pairs, st);
 }
 
+// Tiles of 64 columns for dW's n.
+static bool narrow(int N) { return N <= lin::kBN / 2; }
 // k may be cut into slices (dW).
 template <int SA, bool MNA, int SB, bool MNB>
 static cudaError_t launch_slices(const lin::Params& p, int pairs, cudaStream_t st)
 {
-    return p.a.vec && p.b.vec ? launch_lin_as<SA, MNA, SB, MNB, true, false>(p, pairs, st)
-                              : launch_lin_as<SA, MNA, SB, MNB, false, false>(p, pairs, st);
+    const bool vec = p.a.vec && p.b.vec;
+    if (narrow(p.N))
+        return vec ? launch_lin_as<SA, MNA, SB, MNB, true, false, true>(p, pairs, st)
+                   : launch_lin_as<SA, MNA, SB, MNB, false, false, true>(p, pairs, st);
+    return vec ? launch_lin_as<SA, MNA, SB, MNB, true, false>(p, pairs, st)
+               : launch_lin_as<SA, MNA, SB, MNB, false, false>(p, pairs, st);
 }
 
 // Workspace of the weight gradient: the slices' partial tiles.
 static int weight_ld(int C) { return (C + 7) & ~7; }
 static lin::Params weight_params(int T, int C, int d)
 {
-    lin::Params p = lin_params(d, C, T);
+    lin::Params p = lin_params(d, C, T, narrow(C));
     plan_slices(p, std::max(1, num_sms() / 2));
     return p;
 }
@@ -442,7 +448,7 @@ static beam_status_t check_linear(int T, int C, int d, const void* g, int dtype,
     if (T < 0 || T > (1 << 30)) FAIL_ARG("T=%d outside [0, 2^30]", T);
     if (C < 1 || C > kMaxLogits) FAIL_ARG("C=%d must be in [1, %d]", C, kMaxLogits);
     if (d < 1 || d > kMaxWidth) FAIL_ARG("d=%d must be in [1, %d]", d, kMaxWidth);
-    if (ceil_div(T, lin::BM) * ceil_div(d, lin::BN) > (1LL << 30))
+    if (ceil_div(T, lin::BM) * ceil_div(d, lin::kBN) > (1LL << 30))
         FAIL_ARG("T=%d rows of %d values are too many", T, d);
     return check_matrix("dlogits", g, dtype, false, T, C, ldg);
 }

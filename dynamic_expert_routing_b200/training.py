@@ -4,9 +4,9 @@ linear backward.  Every step runs in the library's kernels; the native module _t
 (csrc/binding.cpp) checks the tensors, allocates the outputs and calls the library.
 
 Each call runs on the current stream of its tensors' device, or on `stream`, for which its
-outputs and scratch are then allocated; the tensors of a returned dict share one allocation.  Tensors that a call cannot take raise ValueError
-(TypeError where a tensor is expected and something else given), a refusal by the library
-BeamError.
+outputs and scratch are then allocated; the tensors of a returned dict share one allocation.
+Tensors that a call cannot take raise ValueError (TypeError where a tensor is expected and
+something else given), a refusal by the library BeamError.
 """
 from __future__ import annotations
 
