@@ -13,7 +13,8 @@
 // its own (the small ones share another), and every kChain steps of 64 the accumulators are
 // drained into float32 sums in registers, rounded to nearest.
 //
-// One kernel computes out[m][n] = sum_k A(m, k) B(n, k) on 256 x 128 tiles (256 x 64 for dW of up to 64 logits), 64 of k per step:
+// One kernel computes out[m][n] = sum_k A(m, k) B(n, k) on 256 x 128 tiles (256 x 64 for dW of up to 64
+// logits), 64 of k per step:
 //   dW: m = d, n = c, k = t: A and B lie in memory with m, n contiguous ("MN-major");
 //   dx: m = t, n = d, k = c: k contiguous ("K-major"; MN-major for a repacked W [C][D]).
 // Two CTAs share a tile (cta_group::2): each converts its 128 rows of A and half of B, so an operand
