@@ -318,7 +318,7 @@ balance_grad_kernel(const T* __restrict__ logits, long long ldl, int n_tok, int 
                     const float* __restrict__ d_l, float* __restrict__ out)
 {
     constexpr int R = 32 / LPR;
-    __shared__ float s_rows[kBalWarps][R * 2 * LPR * kBalPer];
+    __shared__ __align__(16) float s_rows[kBalWarps][R * 2 * LPR * kBalPer];   // read as float4
     __shared__ int s_act;
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane % LPR;
