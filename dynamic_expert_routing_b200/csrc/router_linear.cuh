@@ -22,19 +22,20 @@
 // not bf16 in memory, so TMA could not bring them.  16 warps per CTA write them into shared memory in
 // the 128-byte-swizzled layout that tcgen05.mma reads (a block of rows of 128 bytes; the major-ness
 // is a bit of the instruction descriptor); each thread loads the next step's piece as it converts
-// this one's.  One warp of the first CTA issues the MMAs of both; 8 warps in each drain its rows'
-// accumulators from TMEM (two sets, so that a drain overlaps the next steps) and store.  The grid is
+// this one's.  One warp of the first CTA issues the MMAs of both (two of the second pass on what its warps
+// have ready); 8 warps in each drain its rows' accumulators from TMEM (two sets, so that a drain overlaps
+// the next steps) and store.  The grid is
 // persistent; when the tiles are fewer than the CTA pairs, k is cut into slices whose partial tiles
 // lin_reduce_kernel adds in order.  Where k is short (dx: k = c), a pair converts its rows of A once, keeps
 // them in shared memory and walks a range of n with B alone in the ring.
 // Every wait is bounded: when one runs out, the kernel's outputs are set to NaN.
 //
 // Measured on B200 (device time):
-//   dW 8192 x 1536 x 424, float32 G: 38 us, 280 TFLOP/s of dW's own operations, 0.84 PFLOP/s with the limbs;
+//   dW 8192 x 1536 x 424, float32 G: 38.6 us, 276 TFLOP/s of dW's own operations, 0.83 PFLOP/s with the limbs;
 //     unsliced 92 us.  What bounds it is the loaders' work per step (converting and storing 40 KB per CTA):
-//     the MMAs alone take 20 of the 38 us.  1003 x 2048 x 128, bf16 G: 8.7 us (unsliced 12.2).
-//   dx 8192 x 2048 x 128, float32 G, bf16 W: 19.5 us, 67 MB written (floor 11 us at the copy rate); with A
-//     converted again for every n tile 34 us.  8192 x 1536 x 424 (A too long to stay): 55 us, bf16 G 25 us.
+//     the MMAs alone take 20 of them.  1003 x 2048 x 128, bf16 G: 9.1 us (unsliced 12.2).
+//   dx 8192 x 2048 x 128, float32 G, bf16 W: 19.9 us, 67 MB written (floor 11 us at the copy rate); with A
+//     converted again for every n tile 34 us.  8192 x 1536 x 424 (A too long to stay): 55 us, bf16 G 24 us.
 //   Error against 64 bits at 8192 x 1536 x 424: 1.1e-7; with the accumulator drained every 16 steps 2.1e-7,
 //     never 3.0e-6 (2.3e-6 of it towards zero), with one accumulator for all products 8.5e-7.
 #pragma once
@@ -364,10 +365,12 @@ lin_gemm_kernel(const __grid_constant__ Params p)
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
-        // full and tempty are used in CTA 0 only, by the warps of both CTAs; empty and tfull are signalled
-        // in both by the MMAs' completion
-        for (int s = 0; s < ST; ++s) { tc::mbar_init(full_bar(s), 2 * kLoadWarps); tc::mbar_init(empty_bar(s), 1); }
-        for (int a = 0; a < 2; ++a) { tc::mbar_init(tfull_bar(a), 1); tc::mbar_init(tempty_bar(a), 2 * kEpiWarps); }
+        // full and tempty take the arrivals of the CTA's own warps, and in CTA 0 one more: a warp of CTA 1
+        // passes on its own barrier's completed phases.  empty and tfull are signalled in both
+        // CTAs by the MMAs' completion.
+        const int other = rank == 0 ? 1 : 0;
+        for (int s = 0; s < ST; ++s) { tc::mbar_init(full_bar(s), kLoadWarps + other); tc::mbar_init(empty_bar(s), 1); }
+        for (int a = 0; a < 2; ++a) { tc::mbar_init(tfull_bar(a), 1); tc::mbar_init(tempty_bar(a), kEpiWarps + other); }
         tc::mbar_init(drain_bar, 1);
         tc::mbar_init(afree_bar, 1);
         *abort_flag = 0;
@@ -485,7 +488,7 @@ lin_gemm_kernel(const __grid_constant__ Params p)
             else body(r, std::false_type());
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive_cluster(full_bar(s), 0);
+            if (lane == 0) tc::mbar_arrive(full_bar(s));
             if (++s == ST) { s = 0; ph ^= 1u; }
             return true;
         };
@@ -518,9 +521,10 @@ lin_gemm_kernel(const __grid_constant__ Params p)
                 for (int i = 0, step = t.s0; i < total; ++i) {
                     const uint32_t d0 = tmem_base + (uint32_t)(buf * ACC * BN);
                     if (at == 0) {
-                        if (!tc::mbar_wait(tempty_bar(buf), bph ^ 1u, abort_flag)) { ok = false; break; }
+                        if (!tc::mbar_wait<true>(tempty_bar(buf), bph ^ 1u, abort_flag)) { ok = false; break; }
                     }
-                    if (!tc::mbar_wait(full_bar(s), ph, abort_flag)) { ok = false; break; }
+                    if (!tc::mbar_wait<true>(full_bar(s), ph, abort_flag)) { ok = false; break; }
+                    tc::fence_acquire_shared();
                     tc::tc_fence_after();
                     const uint64_t sa = da + (uint32_t)(RES ? step * (LA * kLimbA >> 4) : s * (kStage >> 4));
                     const uint64_t sb = db + (uint32_t)(s * (kStage >> 4));
@@ -572,6 +576,27 @@ lin_gemm_kernel(const __grid_constant__ Params p)
                 while (!tc::mbar_try_wait(drain_bar, 0) && tc::globaltimer() - t0 < tc::kWaitLimitNs) {}
             }
             __syncwarp();
+        } else if (rank == 1 && warp <= kMmaWarp + 1 && lane == 0) {
+            // -------------------------------------------- CTA 1: two threads pass on to the MMA issuer in CTA 0
+            // what the loaders (the first) and the epilogue (the second) have completed.  A release at cluster scope
+            // alone orders the issuer behind another CTA's threads (a local arrival's ends with the CTA); a loader's
+            // own would wait for the loads of its next step, these threads have none in flight: dW 8192 x 1536 x
+            // 424 38.6 us, with the loaders' own 42.  A phase is passed on before its barrier can complete the
+            // next, which needs the MMAs behind this arrival.
+            const bool steps = warp == kMmaWarp;
+            int left = 0;
+            Unit t;
+            for (int u = pair; get_unit<RES>(p, u, t); u += pairs)
+                left += (t.nt1 - t.nt) * (steps ? t.s1 - t.s0 : (t.s1 - t.s0 + kChain - 1) / kChain);
+            const uint32_t first = steps ? full_bar(0) : tempty_bar(0), end = steps ? full_bar(ST) : tempty_bar(2);
+            uint32_t bar = first, ph = 0;
+            for (; left > 0 && tc::mbar_wait(bar, ph, abort_flag); --left) {
+                tc::tc_fence_after();
+                tc::tc_fence_before();
+                tc::fence_release_shared();
+                tc::mbar_arrive_cluster(bar, 0);
+                if ((bar += 8u) == end) { bar = first; ph ^= 1u; }
+            }
         }
     } else {
         // ------------------------------------------------ epilogue: TMEM -> float32 sums -> global
@@ -604,7 +629,7 @@ lin_gemm_kernel(const __grid_constant__ Params p)
                     }
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive_cluster(tempty_bar(buf), 0);
+                if (lane == 0) tc::mbar_arrive(tempty_bar(buf));
                 if (++buf == 2) { buf = 0; bph ^= 1u; }
             }
             if (!ok)

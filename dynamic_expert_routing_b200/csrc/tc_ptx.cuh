@@ -35,14 +35,26 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
         : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
+// The same for a phase that arrivals of another CTA complete: it orders execution alone (mbar_arrive_cluster).
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
 // Bounded wait: false when the abort flag is raised elsewhere or the time limit passes (then
 // this thread raises the flag itself).
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                           unsigned long long limit_ns = kWaitLimitNs) {
-    if (mbar_try_wait(bar, parity)) return true;
+    auto done = [&]() -> bool { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+    if (done()) return true;
     const unsigned long long t0 = globaltimer();
     while (true) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (done()) return true;
         if (*abort_flag) return false;
         if (globaltimer() - t0 > limit_ns) {
             *abort_flag = 1;
@@ -97,16 +109,23 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrives at the barrier at `bar`'s place in CTA `rank` of the cluster.  What the arrival announces
-// (shared memory behind a proxy fence, TMEM read behind a tcgen05 fence) is read by the
-// tensor cores, so the arrival's default scope is enough; a release at cluster scope would make the
-// warp wait for every load it has in flight.
+// Arrives at the barrier at `bar`'s place in CTA `rank` of the cluster.  Arrival and wait
+// (mbar_try_wait_cluster) order execution at cluster scope and nothing else; what they announce has fences of
+// its own: TMEM accesses the tcgen05 fences, shared memory the pair below.  (A releasing arrival would also
+// order global accesses, and wait for every load that its warp has in flight.)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar, uint32_t rank) {
     asm volatile(
         "{\n\t.reg .b32 a;\n\t"
         "mapa.shared::cluster.u32 a, %0, %1;\n\t"
-        "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}"
+        "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [a];\n\t}"
         ::"r"(bar), "r"(rank) : "memory");
+}
+// Release and acquire at cluster scope of shared memory alone: the releasing CTA's own, and the cluster's.
+__device__ __forceinline__ void fence_release_shared() {
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void fence_acquire_shared() {
+    asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
 }
 // Signals `bar` of both CTAs when the MMAs issued so far have finished.
 __device__ __forceinline__ void tc_commit_pair(uint32_t bar) {

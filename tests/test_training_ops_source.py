@@ -29,3 +29,18 @@ def test_shared_arrays_read_as_vectors_are_aligned():
                     found += 1
                     assert align, f"{name}: {array} is accessed as a 16-byte vector and only 4-byte aligned"
     assert found
+
+
+def test_arrivals_in_another_cta_have_cluster_scope():
+    """An mbarrier arrival or wait without a scope has the CTA's, which orders nothing between two CTAs: an
+    arrival at a barrier of another CTA says .cluster, the shared memory that it announces is released and acquired
+    at cluster scope, and the MMA issuer's waits for another CTA's phases are the cluster ones."""
+    ptx = code("tc_ptx.cuh")
+    remote = re.findall(r"mbarrier\.arrive[\w.]*shared::cluster", ptx)
+    assert remote and all(re.match(r"mbarrier\.arrive\.(release|relaxed)\.cluster\.", r) for r in remote), remote
+    lin = code("router_linear.cuh")
+    arrivals = [m.start() for m in re.finditer(r"mbar_arrive_cluster\(", lin)]
+    assert arrivals and all("fence_release_shared();" in lin[max(0, at - 120):at] for at in arrivals)
+    issuer = lin[lin.index("kMmaWarp && rank == 0"):lin.index("tc_mma_f16_pair")]
+    waits = re.findall(r"mbar_wait(<true>)?\((?:full|tempty)_bar", issuer)
+    assert len(waits) == 2 and all(waits) and "fence_acquire_shared();" in issuer
