@@ -6,9 +6,10 @@
 // Both run on the tensor cores (tcgen05, bf16 operands, fp32 accumulation) and keep float32's
 // precision.  A checkpoint value q 2^k and a bf16 value are bf16 operands as they are.  A float32
 // value is the exact sum of three bf16 numbers cut from its 24 significant bits, 8 at a time (its
-// upper half; the upper half of the rest; the rest), and the product of two operands is taken limb by limb: all
-// pairs (i, j) with i + j at most max(limbs) - 1, the terms left out being below 2^-24 of the
-// product.  The tensor cores add into their accumulator with truncation, an error of one sign that
+// upper half; the upper half of the rest; the rest): cut, not rounded, the second reaches 2^-7 of the value and the
+// third 2^-15.  The product of two operands is taken limb by limb, all pairs but the two third limbs', which
+// stays below 2^-30 of it (leaving out the pairs of a second and a third limb too, 2^-22 each and of one
+// sign, would cost a float32 x float32 product 2^-21).  The tensor cores add into their accumulator with truncation, an error of one sign that
 // grows with the number of additions: the leading product therefore has an accumulator of
 // its own (the small ones share another), and every kChain steps of 64 the accumulators are
 // drained into float32 sums in registers, rounded to nearest.
@@ -540,7 +541,7 @@ lin_gemm_kernel(const __grid_constant__ Params p)
                             for (int i = 0; i < LA; ++i)
 #pragma unroll
                                 for (int j = 0; j < LB; ++j) {
-                                    if (i + j >= (LA > LB ? LA : LB)) continue;
+                                    if (i + j > 3) continue;   // below 2^-30 of the product
                                     const uint64_t ad = sa + (uint32_t)(i * (kLimbA >> 4) + kk * KA);
                                     const uint64_t bd = sb + (uint32_t)(j * (kLimbB >> 4) + kk * KB);
                                     const bool add = kk > 0 || at > 0;
