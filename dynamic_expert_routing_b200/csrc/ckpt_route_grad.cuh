@@ -3,7 +3,7 @@
 // from a checkpoint in slot order [T K][D] instead of the handle's last forward.
 //   s_tk = <dy_t, Y_tk>;  over a decision's tokens (one token, or a segment of S):
 //   dg_k = m_k sum s_tk, m_k = [l_k >= 0];  dmh_k = g_k sum s_tk + n reg
-//   d_l_k = dmh_k sigmoid(l_k)(1 - sigmoid(l_k));  d_r_k = g_k (dg_k - sum_j g_j dg_j)
+//   d_l_k = dmh_k sigmoid(l_k) sigmoid(-l_k);  d_r_k = g_k (dg_k - sum_j g_j dg_j)
 // The decision's gradients go to its first token; the others of a segment get 0.
 // HBM-bound: one byte per expert-output value and dy once; at K = 16 the unpacking (a byte permute
 // and half an add per value) and the multiply-adds (half an instruction) are within a factor of two of the
@@ -28,9 +28,8 @@ __device__ __forceinline__ void slot_grads(bool on, float run, float g, float l,
 {
     const float dg = (on && l >= 0.f) ? run : 0.f;
     const float c = warp_sum(on ? g * dg : 0.f);
-    const float sg = sigmoid_f(l);
     gr = g * (dg - c);
-    gl = fmaf(run, g, (float)n * reg) * (sg * (1.f - sg));
+    gl = fmaf(run, g, (float)n * reg) * (sigmoid_f(l) * sigmoid_f(-l));   // 1 - sigmoid(l) would cancel for a large l
 }
 
 // Sums v[0..N) over the warp's lanes: afterwards lane k (k < N) holds the total of v[k].  Each

@@ -68,3 +68,29 @@ def test_layer_input_grad_product_of_two_float32_numbers():
                                           ctypes.c_void_p(dx.data_ptr()), D,
                                           ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
     assert (np.abs(np64(dx) - want) / np.abs(want)).max() <= PRODUCT
+
+
+# ------------------------------------------------------------------------------ slot gradients
+@pytest.mark.parametrize("seg", [0, 4])
+@pytest.mark.parametrize("K", [2, 11, 32])
+def test_mask_gradient_of_confident_masks(K, seg):
+    """sigmoid'(l) far from 0: the dots are exact (small integers), so d_mask_logit has the roundings of the gate's
+    product (u), of sigma(l) and sigma(-l) (an exponential of 2 steps, 4 u, an addition and a division: 6 u
+    at most, 2 u where the exponential is small) and of two more products: 11 u, 16 u allowed."""
+    T, D, S = 24, 32, max(1, seg)
+    r = np.random.default_rng(K)
+    lead = np.arange(T) // S * S
+    l = np.resize(np.float32([-80, -20, -10, -1, 0, 1, 10, 14, 17, 20, 25, 40, 80]), (T, K))[lead]
+    gate = r.integers(1, 256, (T, K)).astype(np.float32)[lead] / 256
+    y, dy = r.integers(-8, 9, (T * K, D)).astype(np.float32), r.integers(1, 5, (T, D)).astype(np.float32)
+    y[:, 0] = 8                                             # exact in steps of 2^-3, and no dot is 0
+    y[:, 1:] = np.abs(y[:, 1:])
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    out = beam().checkpoint_route_grad(beam().checkpoint_save(t(y)), t(gate), t(l), t(dy), segment_len=seg)
+    s = np.einsum("tkd,td->tk", y.reshape(T, K, D).astype(np.float64), dy.astype(np.float64))
+    np.testing.assert_array_equal(np64(out["dghat"]), s)
+    l64, want = l.astype(np.float64), np.zeros((T, K))
+    e = np.exp(-np.abs(l64))
+    for i in range(0, T, S):
+        want[i] = s[i:i + S].sum(0) * gate[i] * (e / (1 + e) ** 2)[i]
+    np.testing.assert_allclose(np64(out["d_mask_logit"]), want, rtol=16 * U, atol=0)
