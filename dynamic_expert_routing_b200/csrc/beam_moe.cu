@@ -2656,6 +2656,8 @@ beam_status_t beam_moe_router_input_grad(beam_moe_t* h, const float* dlogits, in
     g_err[0] = 0;
     if (!h) return fail(BEAM_ERR_INVALID_ARG, "handle is NULL");
     BEAM_TRY(beam_host_input_grad_rows(dlogits, ld_dlogits, T, h->n2E, h->wrm, h->cfg.dtype, h->D, h->D, dx, ld_dx, stream));
+    // the handle's router matrices are read until here: a destroy waits for it
+    BEAM_CUDA(cudaEventRecord(h->done, static_cast<cudaStream_t>(stream)));
     return BEAM_OK;
 }
 

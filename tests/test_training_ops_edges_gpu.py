@@ -94,3 +94,35 @@ def test_mask_gradient_of_confident_masks(K, seg):
     for i in range(0, T, S):
         want[i] = s[i:i + S].sum(0) * gate[i] * (e / (1 + e) ** 2)[i]
     np.testing.assert_allclose(np64(out["d_mask_logit"]), want, rtol=16 * U, atol=0)
+
+
+# ------------------------------------------------------------------------------ a layer's calls
+def small_layer(T, **kw):
+    spec = synth.LayerSpec("small", 512, 16, 4, 256, **kw)
+    w = {k: v.cuda().contiguous() for k, v in synth.make_layer(spec, seed=0).items() if isinstance(v, torch.Tensor)}
+    return beam().BeamMoE(w, spec.top_k, max_tokens=T, segment_len=spec.segment_len), synth.make_tokens(spec, T, seed=0).cuda()
+
+
+def test_the_handle_waits_for_its_input_gradient():
+    """beam_moe_router_input_grad reads the handle's router matrices: it belongs to the pending work that
+    beam_moe_destroy (and beam_moe_host_wait, which waits for the same event) waits for."""
+    layer, _ = small_layer(8)
+    g, dx = torch.ones((8, 32), device="cuda"), torch.empty((8, 512), device="cuda")
+    st, before = torch.cuda.Stream(), torch.cuda.Event()
+    lib = beam().load()
+
+    def call():
+        assert lib.beam_moe_router_input_grad(layer._h, ctypes.c_void_p(g.data_ptr()), 32, 8, ctypes.c_void_p(dx.data_ptr()),
+                                              512, ctypes.c_void_p(st.cuda_stream)) == 0
+
+    torch.cuda.synchronize()
+    call()                                      # the first call loads the kernel
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(400_000_000)          # about 0.2 s
+        before.record()
+    call()
+    assert not before.query()                   # the stream is still asleep
+    layer.host_wait()
+    assert before.query()
+    torch.cuda.synchronize()
