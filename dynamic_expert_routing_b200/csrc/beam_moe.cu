@@ -2610,6 +2610,16 @@ beam_status_t beam_moe_backward_router(beam_moe_t* h, const void* x, const float
 }
 
 // ---------------------------------------------------------------- checkpoint of a training forward
+// The handle's buffers are read up to here on `st`: a destroy waits for it.  A call that is being captured
+// leaves the event alone, which would be the graph's and could not be waited for.
+static cudaError_t mark_done(beam_moe* h, cudaStream_t st)
+{
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    const cudaError_t e = cudaStreamIsCapturing(st, &cs);
+    if (e != cudaSuccess || cs != cudaStreamCaptureStatusNone) return e;
+    return cudaEventRecord(h->done, st);
+}
+
 beam_status_t beam_moe_checkpoint(beam_moe_t* h, int32_t T, int8_t* y_q, uint8_t* y_scale, int32_t* topk_id,
                                   float* gate, float* mask_logit, float* logits, void* stream)
 {
@@ -2645,8 +2655,7 @@ beam_status_t beam_moe_checkpoint(beam_moe_t* h, int32_t T, int8_t* y_q, uint8_t
         BEAM_CUDA(launch_free(ckpt_logits_kernel, dim3((unsigned)ceil_div(Tr * h->n2E, 256)), dim3(256), 0, st,
                               (const float*)h->L, h->l_splits, h->l_stride, h->ldL, Tr, h->n2E, logits));
     }
-    // the handle's buffers are read until here: a destroy waits for it
-    BEAM_CUDA(cudaEventRecord(h->done, st));
+    BEAM_CUDA(mark_done(h, st));
     return BEAM_OK;
 }
 
@@ -2656,8 +2665,7 @@ beam_status_t beam_moe_router_input_grad(beam_moe_t* h, const float* dlogits, in
     g_err[0] = 0;
     if (!h) return fail(BEAM_ERR_INVALID_ARG, "handle is NULL");
     BEAM_TRY(beam_host_input_grad_rows(dlogits, ld_dlogits, T, h->n2E, h->wrm, h->cfg.dtype, h->D, h->D, dx, ld_dx, stream));
-    // the handle's router matrices are read until here: a destroy waits for it
-    BEAM_CUDA(cudaEventRecord(h->done, static_cast<cudaStream_t>(stream)));
+    BEAM_CUDA(mark_done(h, static_cast<cudaStream_t>(stream)));
     return BEAM_OK;
 }
 

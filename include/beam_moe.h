@@ -612,6 +612,8 @@ beam_status_t beam_router_input_grad(const void *dlogits_dev, int32_t dtype, int
  * beam_router_weight_grad with parts = 2, and beam_moe_router_input_grad:
  *   dx_dev [T][D] float32, rows ld_dx elements apart, = dlogits [W_r | W_m]^T with the handle's own
  *   router matrices, for dlogits_dev [T][2E] float32, rows ld_dlogits elements apart.
+ * Both calls may be captured into a graph; its replays, unlike the calls themselves, are not work that
+ * beam_moe_destroy waits for.
  */
 beam_status_t beam_moe_checkpoint(beam_moe_t *h, int32_t T, int8_t *y_q_dev, uint8_t *y_scale_dev,
                                   int32_t *topk_id_dev, float *gate_dev, float *mask_logit_dev,

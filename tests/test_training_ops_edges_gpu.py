@@ -126,3 +126,28 @@ def test_the_handle_waits_for_its_input_gradient():
     layer.host_wait()
     assert before.query()
     torch.cuda.synchronize()
+
+
+def test_layer_calls_captured_into_a_graph():
+    """checkpoint and backward_checkpoint captured and replayed give the eager results, and the handle still answers."""
+    T = 96
+    layer, x = small_layer(T)
+    dy = rnd(1, T, 512).cuda()
+    layer.forward(x, train=True)
+
+    def both():
+        c = layer.checkpoint(x)
+        return dict(layer.backward_checkpoint(c, dy, reg_scale=0.2), q=c["y"]["q"], logits=c["logits"])
+    want = both()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for k, v in want.items():
+        assert torch.equal(got[k], v), k
+    assert layer.stats()["tokens"] == T
+    np.testing.assert_array_equal(layer.routing(T)["topk_id"].shape, (T, layer.top_k))
+    layer.host_wait()
