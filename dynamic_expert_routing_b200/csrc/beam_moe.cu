@@ -2647,6 +2647,7 @@ beam_status_t beam_moe_checkpoint(beam_moe_t* h, int32_t T, int8_t* y_q, uint8_t
                                    yr.splits, yr.stride, (const int*)h->inv, rows, h->D, nb, y_q, y_scale)
                      : launch_free(ckpt_experts_kernel<float>, grid, dim3(kCkptThreads), 0, st, (const float*)yr.base,
                                    yr.splits, yr.stride, (const int*)h->inv, rows, h->D, nb, y_q, y_scale));
+    ++h->launches;
     BEAM_CUDA(cudaMemcpyAsync(topk_id, h->topk_id, rows * 4, cudaMemcpyDeviceToDevice, st));
     BEAM_CUDA(cudaMemcpyAsync(gate, h->gate, rows * 4, cudaMemcpyDeviceToDevice, st));
     BEAM_CUDA(cudaMemcpyAsync(mask_logit, h->mlogit, rows * 4, cudaMemcpyDeviceToDevice, st));
@@ -2654,6 +2655,7 @@ beam_status_t beam_moe_checkpoint(beam_moe_t* h, int32_t T, int8_t* y_q, uint8_t
         const long long Tr = ceil_div(T, h->S);
         BEAM_CUDA(launch_free(ckpt_logits_kernel, dim3((unsigned)ceil_div(Tr * h->n2E, 256)), dim3(256), 0, st,
                               (const float*)h->L, h->l_splits, h->l_stride, h->ldL, Tr, h->n2E, logits));
+        ++h->launches;
     }
     BEAM_CUDA(mark_done(h, st));
     return BEAM_OK;
@@ -2665,6 +2667,7 @@ beam_status_t beam_moe_router_input_grad(beam_moe_t* h, const float* dlogits, in
     g_err[0] = 0;
     if (!h) return fail(BEAM_ERR_INVALID_ARG, "handle is NULL");
     BEAM_TRY(beam_host_input_grad_rows(dlogits, ld_dlogits, T, h->n2E, h->wrm, h->cfg.dtype, h->D, h->D, dx, ld_dx, stream));
+    if (T > 0) ++h->launches;
     BEAM_CUDA(mark_done(h, static_cast<cudaStream_t>(stream)));
     return BEAM_OK;
 }

@@ -151,3 +151,13 @@ def test_layer_calls_captured_into_a_graph():
     assert layer.stats()["tokens"] == T
     np.testing.assert_array_equal(layer.routing(T)["topk_id"].shape, (T, layer.top_k))
     layer.host_wait()
+
+
+def test_launch_count_includes_the_checkpoint_calls():
+    layer, x = small_layer(32)
+    layer.forward(x, train=True)
+    n = layer.launch_count()
+    c = layer.checkpoint(x)                     # expert outputs, logits
+    assert layer.launch_count() == n + 2
+    layer.backward_checkpoint(c, torch.ones((32, 512), device="cuda"))
+    assert layer.launch_count() == n + 3        # dx; the other operators belong to no handle
