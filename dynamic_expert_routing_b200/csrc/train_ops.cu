@@ -74,7 +74,8 @@ struct BalArgs {
     const uint8_t* valid; const int32_t* cu; int n_seq;
 };
 
-static beam_status_t check_balance(const BalArgs& a)
+// ids: whether topk_id is read.
+static beam_status_t check_balance(const BalArgs& a, bool ids)
 {
     if (a.T < 0 || a.T > (1 << 30)) FAIL_ARG("T=%d outside [0, 2^30]", a.T);
     if (a.E < 1 || a.E > kMaxExperts) FAIL_ARG("E=%d must be in [1, %d]", a.E, kMaxExperts);
@@ -83,7 +84,7 @@ static beam_status_t check_balance(const BalArgs& a)
     if (a.cu ? (a.n_seq < 1 || a.n_seq > 65536) : a.n_seq != 0)
         FAIL_ARG("n_seq=%d: 1 to 65536 sequences with cu_seqlens, 0 without", a.n_seq);
     TRY(check_matrix("logits", a.logits, a.dtype, false, a.T, a.E, a.ldl));
-    if (a.T > 0 && !a.topk) FAIL_ARG("topk_id is NULL");
+    if (ids && a.T > 0 && !a.topk) FAIL_ARG("topk_id is NULL");
     if (misaligned(a.topk, 4) || misaligned(a.cu, 4)) FAIL_ARG("the int32 arrays must be 4-byte aligned");
     return BEAM_OK;
 }
@@ -173,7 +174,7 @@ beam_status_t beam_balance_forward(const void* logits, int32_t dtype, int32_t T,
 {
     beam_host_clear_error();
     const BalArgs a{logits, dtype, T, E, ld_logits, topk_id, K, valid, cu_seqlens, n_seq};
-    TRY(check_balance(a));
+    TRY(check_balance(a, true));
     if (!loss || !prob || !counts || !tokens) FAIL_ARG("an output pointer is NULL");
     if (misaligned(loss, 4) || misaligned(prob, 4) || misaligned(counts, 4) || misaligned(tokens, 4))
         FAIL_ARG("the outputs must be 4-byte aligned");
@@ -204,7 +205,7 @@ beam_status_t beam_balance_backward(const void* logits, int32_t dtype, int32_t T
 {
     beam_host_clear_error();
     const BalArgs a{logits, dtype, T, E, ld_logits, topk_id, K, valid, cu_seqlens, n_seq};
-    TRY(check_balance(a));
+    TRY(check_balance(a, d_gate_logit != nullptr));
     if (!std::isfinite(scale)) FAIL_ARG("scale must be finite");
     if (!d_gate_logit != !d_mask_logit) FAIL_ARG("d_gate_logit and d_mask_logit come together");
     if (T > 0 && (!counts || !tokens || !dlogits)) FAIL_ARG("counts, tokens and dlogits are required");

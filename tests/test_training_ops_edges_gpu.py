@@ -161,3 +161,24 @@ def test_launch_count_includes_the_checkpoint_calls():
     assert layer.launch_count() == n + 2
     layer.backward_checkpoint(c, torch.ones((32, 512), device="cuda"))
     assert layer.launch_count() == n + 3        # dx; the other operators belong to no handle
+
+
+def test_balance_backward_reads_topk_only_with_slot_gradients():
+    b = beam()
+    T, E, K = 37, 12, 3
+    logits = rnd(0, T, E).cuda()
+    ids = torch.topk(logits, K, dim=1).indices.int()
+    bal = b.balance_loss(logits, ids)
+    want = b.balance_loss_backward(logits, ids, bal, scale=0.5)
+    got = torch.empty_like(want)
+    lib, p = b.load(), lambda t: ctypes.c_void_p(t.data_ptr())
+    slots = torch.zeros((T, K), device="cuda")
+
+    def call(gr, gl, out):
+        return lib.beam_balance_backward(p(logits), 0, T, E, E, None, K, None, None, 0, p(bal["counts"]), p(bal["tokens"]),
+                                         ctypes.c_float(0.5), gr, gl, p(out),
+                                         ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert call(None, None, got) == 0
+    assert torch.equal(got, want)
+    assert call(p(slots), p(slots), torch.empty((T, 2 * E), device="cuda")) == 1        # BEAM_ERR_INVALID_ARG
+    torch.cuda.synchronize()
