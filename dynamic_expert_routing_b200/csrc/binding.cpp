@@ -170,7 +170,11 @@ Groups groups(const Tensor& logits, const Tensor& topk, const Opt& valid, const 
     Groups g;
     g.K = topk.size(1);
     g.ids = static_cast<const int32_t*>(array("topk_id", topk, at::kInt, {logits.size(0), g.K}, logits));
-    g.valid = valid ? static_cast<const uint8_t*>(array("valid", *valid, at::kByte, {logits.size(0)}, logits)) : nullptr;
+    g.valid = nullptr;
+    if (valid) {   // a bool is a byte of 0 or 1
+        const at::ScalarType type = valid->scalar_type() == at::kBool ? at::kBool : at::kByte;
+        g.valid = static_cast<const uint8_t*>(array("valid", *valid, type, {logits.size(0)}, logits));
+    }
     g.cu = nullptr;
     g.n = 0;
     if (cu) {

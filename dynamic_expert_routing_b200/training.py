@@ -44,7 +44,7 @@ def balance_loss(logits: torch.Tensor, topk_id: torch.Tensor, valid: torch.Tenso
                  cu_seqlens: torch.Tensor | None = None, stream=None) -> dict:
     """The load-balance loss of router logits [T][E] (float32 or bfloat16; rows may be strided)
     and their Top-K assignments topk_id [T][K] int32, over the whole batch or per packed sequence
-    (cu_seqlens [n_seq + 1] int32), leaving out the tokens with valid [T] uint8 = 0.  Returns
+    (cu_seqlens [n_seq + 1] int32), leaving out the tokens with valid [T] (uint8 or bool) = 0.  Returns
     loss (a float32 scalar tensor), counts [G][E] int32 (slots per expert), prob [G][E] float32
     (mean router probabilities) and tokens [G] int32.  See beam_balance_forward."""
     if stream is not None:

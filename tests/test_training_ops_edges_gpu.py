@@ -182,3 +182,19 @@ def test_balance_backward_reads_topk_only_with_slot_gradients():
     assert torch.equal(got, want)
     assert call(p(slots), p(slots), torch.empty((T, 2 * E), device="cuda")) == 1        # BEAM_ERR_INVALID_ARG
     torch.cuda.synchronize()
+
+
+def test_balance_takes_bool_masks():
+    b = beam()
+    T, E, K = 300, 24, 4
+    logits = rnd(0, T, E).cuda()
+    ids = torch.topk(logits, K, dim=1).indices.int()
+    mask = rnd(1, T).cuda() > -0.5
+    byte = mask.to(torch.uint8)
+    want, got = b.balance_loss(logits, ids, valid=byte), b.balance_loss(logits, ids, valid=mask)
+    for k in want:
+        assert torch.equal(got[k], want[k]), k
+    assert torch.equal(b.balance_loss_backward(logits, ids, got, valid=mask),
+                       b.balance_loss_backward(logits, ids, want, valid=byte))
+    with pytest.raises(ValueError):
+        b.balance_loss(logits, ids, valid=mask.float())
