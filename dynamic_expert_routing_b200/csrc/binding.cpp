@@ -75,6 +75,31 @@ void done(int status)
 
 [[noreturn]] void bad(const std::string& msg) { throw py::value_error(msg); }
 
+// A value of a dict that a caller hands in (borrowed).
+PyObject* field(const char* what, const py::dict& d, const py::object& key)
+{
+    PyObject* const v = PyDict_GetItemWithError(d.ptr(), key.ptr());
+    if (!v && PyErr_Occurred()) throw py::error_already_set();
+    if (!v) bad(std::string(what) + " has no '" + key.cast<std::string>() + "'");
+    return v;
+}
+Tensor field_tensor(const char* what, const py::dict& d, const py::object& key)
+{
+    PyObject* const v = field(what, d, key);
+    if (!THPVariable_Check(v))
+        throw py::type_error(std::string(what) + "['" + key.cast<std::string>() + "'] must be a tensor, got " + Py_TYPE(v)->tp_name);
+    return THPVariable_Unpack(v);
+}
+int64_t field_int(const char* what, const py::dict& d, const py::object& key)
+{
+    PyObject* const v = field(what, d, key);
+    if (!PyIndex_Check(v))
+        throw py::type_error(std::string(what) + "['" + key.cast<std::string>() + "'] must be an integer, got " + Py_TYPE(v)->tp_name);
+    const Py_ssize_t n = PyNumber_AsSsize_t(v, nullptr);   // past its range: the nearest end of it
+    if (n == -1 && PyErr_Occurred()) throw py::error_already_set();
+    return n;
+}
+
 // The tensors' device for the call: makes it current, gives its current stream, allocates on it.
 struct On {
     c10::cuda::OptionalCUDAGuard guard;
@@ -212,7 +237,7 @@ Tensor balance_loss_backward(const Tensor& logits, const Tensor& topk, const py:
     const Matrix m = matrix("logits", logits, false);
     const Groups g = groups(logits, topk, valid, cu);
     const int64_t G = std::max<int64_t>(1, g.n);
-    const Tensor c = balance[KEY("counts")].cast<Tensor>(), t = balance[KEY("tokens")].cast<Tensor>();
+    const Tensor c = field_tensor("balance", balance, KEY("counts")), t = field_tensor("balance", balance, KEY("tokens"));
     void* counts = array("balance['counts']", c, at::kInt, {G, m.cols}, logits);
     void* tokens = array("balance['tokens']", t, at::kInt, {G}, logits);
     if (d_gate.has_value() != d_mask.has_value()) bad("d_gate_logit and d_mask_logit come together");
@@ -253,9 +278,9 @@ struct Ckpt {
 Ckpt checkpoint(const py::dict& c)
 {
     Ckpt k;
-    k.t = c[KEY("q")].cast<Tensor>();
-    const Tensor scale = c[KEY("scale")].cast<Tensor>();
-    k.d = c[KEY("d")].cast<int64_t>();
+    k.t = field_tensor("checkpoint", c, KEY("q"));
+    const Tensor scale = field_tensor("checkpoint", c, KEY("scale"));
+    k.d = field_int("checkpoint", c, KEY("d"));
     if (!k.t.is_cuda() || k.t.dim() != 2 || k.d < 1 || k.d > INT32_MAX - kBlock)
         bad("a checkpoint holds CUDA tensors q [rows][..] and scale and a width d >= 1");
     k.rows = k.t.size(0);

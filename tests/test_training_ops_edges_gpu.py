@@ -198,3 +198,14 @@ def test_balance_takes_bool_masks():
                        b.balance_loss_backward(logits, ids, want, valid=byte))
     with pytest.raises(ValueError):
         b.balance_loss(logits, ids, valid=mask.float())
+
+
+def test_a_balance_dict_without_one_of_its_parts():
+    b = beam()
+    logits, ids = rnd(0, 6, 8).cuda(), torch.zeros((6, 2), dtype=torch.int32, device="cuda")
+    bal = b.balance_loss(logits, ids)
+    for key in ("counts", "tokens"):
+        with pytest.raises(ValueError, match=key):
+            b.balance_loss_backward(logits, ids, {k: v for k, v in bal.items() if k != key})
+        with pytest.raises(TypeError, match=key):
+            b.balance_loss_backward(logits, ids, dict(bal, **{key: 3}))
