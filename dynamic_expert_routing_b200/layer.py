@@ -15,7 +15,7 @@ from ._lib import (BEAM_DTYPE_BF16, BEAM_DTYPE_F32, BEAM_MASK_OFF, BEAM_FUSED_DE
                    BEAM_PATH_STREAM, BEAM_PATH_TENSOR, BEAM_TRAIN, BeamConfig, BeamGenConfig,
                    BeamRouting, BeamStats, BeamWeights, check)
 from .training import (CKPT_BLOCK, balance_loss_backward, checkpoint_route_grad, checkpoint_save,
-                       router_weight_grad)
+                       on_stream, router_weight_grad)
 
 _DTYPES = {torch.float32: BEAM_DTYPE_F32, torch.bfloat16: BEAM_DTYPE_BF16}
 _PATHS = {None: 0, "auto": 0, "stream": BEAM_PATH_STREAM, "tensor": BEAM_PATH_TENSOR}
@@ -137,7 +137,7 @@ class BeamMoE:
         [rows][2E] float32 (the first E columns are balance_loss's input).  rows = T, or one per
         segment.  See beam_moe_checkpoint."""
         if stream is not None or (x.is_cuda and x.device.index != torch.cuda.current_device()):
-            with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(x.device):
+            with on_stream(stream, x) if stream is not None else torch.cuda.device(x.device):
                 return self.checkpoint(x)
         if not (x.is_cuda and x.is_contiguous() and x.dtype == self.dtype and x.dim() == 2
                 and x.shape[1] == self.d_model):
@@ -168,7 +168,7 @@ class BeamMoE:
         result is `balance`.  Returns dw_router, dw_mask [D][E], dx [T][D] (float32; with segments 0
         but for the routed rows) and the per-slot dghat, d_gate_logit and d_mask_logit [T][K]."""
         if stream is not None or (dy.is_cuda and dy.device.index != torch.cuda.current_device()):
-            with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dy.device):
+            with on_stream(stream, dy) if stream is not None else torch.cuda.device(dy.device):
                 return self.backward_checkpoint(ckpt, dy, reg_scale, balance, balance_scale, valid,
                                                 cu_seqlens)
         if balance is None and balance_scale != 0.0:

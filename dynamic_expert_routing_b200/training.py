@@ -3,7 +3,7 @@
 linear backward.  Every step runs in the library's kernels; the native module _training
 (csrc/binding.cpp) checks the tensors, allocates the outputs and calls the library.
 
-Each call runs on the current stream of its tensors' device, or on `stream`, for which its
+Each call runs on the current stream of its tensors' device, or on `stream` of that device, for which its
 outputs and scratch are then allocated; the tensors of a returned dict share one allocation.
 Tensors that a call cannot take raise ValueError (TypeError where a tensor is expected and
 something else given), a refusal by the library BeamError.
@@ -35,8 +35,16 @@ def _native():
     return _ops
 
 
+def on_stream(stream, tensor):
+    """The context in which a call on `tensor` runs on `stream`, a stream of the tensor's device."""
+    if isinstance(tensor, torch.Tensor) and tensor.device != stream.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {tensor.device}")
+    return torch.cuda.stream(stream)
+
+
 def _run(name: str, stream, *args):
-    with torch.cuda.stream(stream):
+    first = args[0]
+    with on_stream(stream, first.get("q") if isinstance(first, dict) else first):
         return getattr(_ops or _native(), name)(*args)
 
 

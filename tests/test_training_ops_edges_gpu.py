@@ -209,3 +209,20 @@ def test_a_balance_dict_without_one_of_its_parts():
             b.balance_loss_backward(logits, ids, {k: v for k, v in bal.items() if k != key})
         with pytest.raises(TypeError, match=key):
             b.balance_loss_backward(logits, ids, dict(bal, **{key: 3}))
+
+
+def test_layer_calls_on_a_given_stream():
+    T = 64
+    layer, x = small_layer(T)
+    dy = rnd(2, T, 512).cuda()
+    layer.forward(x, train=True)
+    want = layer.backward_checkpoint(layer.checkpoint(x), dy, reg_scale=0.1)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    torch.cuda._sleep(20_000_000)               # the current stream is busy: nothing may wait for it or run on it
+    layer.forward(x, train=True, stream=st)
+    got = layer.backward_checkpoint(layer.checkpoint(x, stream=st), dy, reg_scale=0.1, stream=st)
+    st.synchronize()
+    for k, v in want.items():
+        assert torch.equal(got[k], v), k
+    torch.cuda.synchronize()

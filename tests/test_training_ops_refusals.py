@@ -29,3 +29,23 @@ def test_a_checkpoint_without_one_of_its_parts(beam, key):
             call(ckpt(**{key: "8"}))
         with pytest.raises(TypeError, match=key):
             call(ckpt(**{key: None}))
+
+
+class OtherStream:
+    """A stream of a device that no tensor here is on."""
+    device = torch.device("cuda", 1)
+    cuda_stream = 0
+
+
+def test_a_stream_of_another_device(beam):
+    """A call runs on its tensors' device; a stream of another one is refused, not passed over."""
+    f, i, st = torch.zeros((4, 8)), torch.zeros((4, 2), dtype=torch.int32), OtherStream()
+    layer = object.__new__(beam.BeamMoE)
+    layer._h = None
+    for call in (lambda: beam.balance_loss(f, i, stream=st), lambda: beam.balance_loss_backward(f, i, {}, stream=st),
+                 lambda: beam.checkpoint_save(f, stream=st), lambda: beam.checkpoint_load(ckpt(), stream=st),
+                 lambda: beam.checkpoint_route_grad(ckpt(), f, f, f, stream=st),
+                 lambda: beam.router_weight_grad(ckpt(), f, stream=st), lambda: beam.router_input_grad(f, f, stream=st),
+                 lambda: layer.checkpoint(f, stream=st), lambda: layer.backward_checkpoint({}, f, stream=st)):
+        with pytest.raises(ValueError, match="stream is on cuda:1"):
+            call()
