@@ -159,20 +159,23 @@ class BeamMoE:
         return out
 
     def backward_checkpoint(self, ckpt: dict, dy: torch.Tensor, reg_scale: float = 0.0,
-                            balance: dict | None = None, balance_scale: float = 0.0,
+                            balance: dict | None = None, balance_scale: float | None = None,
                             valid: torch.Tensor | None = None, cu_seqlens: torch.Tensor | None = None,
                             stream=None) -> dict:
         """backward_router from a checkpoint(), for the upstream gradient dy [T][D] (float32 or
         bfloat16) and reg_scale = dL/dL_reg, plus balance_scale = dL/dL_bal times the gradient of
         balance_loss(ckpt["logits"][:, :E], topk_id of the routed rows, valid, cu_seqlens), whose
-        result is `balance`.  Returns dw_router, dw_mask [D][E], dx [T][D] (float32; with segments 0
-        but for the routed rows) and the per-slot dghat, d_gate_logit and d_mask_logit [T][K]."""
+        result is `balance` (the two are given together).  Returns dw_router, dw_mask [D][E], dx [T][D]
+        (float32; with segments 0 but for the routed rows) and the per-slot dghat, d_gate_logit and
+        d_mask_logit [T][K]."""
         if stream is not None or (dy.is_cuda and dy.device.index != torch.cuda.current_device()):
             with on_stream(stream, dy) if stream is not None else torch.cuda.device(dy.device):
                 return self.backward_checkpoint(ckpt, dy, reg_scale, balance, balance_scale, valid,
                                                 cu_seqlens)
-        if balance is None and balance_scale != 0.0:
+        if balance is None and balance_scale:
             raise ValueError("balance_scale needs the balance loss's result")
+        if balance is not None and balance_scale is None:
+            raise ValueError("balance needs balance_scale = dL/dL_bal")
         T, E, D, S = dy.shape[0], self.n_experts, self.d_model, max(1, self.cfg.segment_len)
         slots = checkpoint_route_grad(ckpt["y"], ckpt["gate"], ckpt["mask_logit"], dy, reg_scale,
                                       self.cfg.segment_len)
@@ -183,7 +186,7 @@ class BeamMoE:
             G = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
             balance = dict(counts=torch.zeros(G, E, dtype=torch.int32, device=dy.device),
                            tokens=torch.zeros(G, dtype=torch.int32, device=dy.device))
-        g = balance_loss_backward(ckpt["logits"][:, :E], ids, balance, balance_scale, valid, cu_seqlens,
+        g = balance_loss_backward(ckpt["logits"][:, :E], ids, balance, balance_scale or 0.0, valid, cu_seqlens,
                                   gr, gl)
         dw = router_weight_grad(ckpt["x"], g, parts=2)
         dx = (torch.empty if S == 1 else torch.zeros)(T, D, dtype=torch.float32, device=dy.device)

@@ -49,3 +49,13 @@ def test_a_stream_of_another_device(beam):
                  lambda: layer.checkpoint(f, stream=st), lambda: layer.backward_checkpoint({}, f, stream=st)):
         with pytest.raises(ValueError, match="stream is on cuda:1"):
             call()
+
+
+def test_balance_and_its_scale_come_together(beam):
+    """A balance result without balance_scale would leave its term out, a scale without a result has no term."""
+    layer = object.__new__(beam.BeamMoE)
+    layer._h, dy = None, torch.zeros((4, 8))
+    with pytest.raises(ValueError, match="balance_scale"):
+        layer.backward_checkpoint({}, dy, balance={})
+    with pytest.raises(ValueError, match="balance_scale"):
+        layer.backward_checkpoint({}, dy, balance_scale=0.5)
