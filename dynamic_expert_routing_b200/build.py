@@ -2,6 +2,7 @@
 side of training.py, _training.so, with g++ against the installed torch."""
 from __future__ import annotations
 
+import importlib.metadata
 import importlib.util
 import os
 import re
@@ -17,6 +18,7 @@ UNITS = [os.path.join(CSRC, f) for f in ("beam_moe.cu", "train_ops.cu")]
 OBJ = os.path.join(HERE, "_build")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 BINDING = os.path.join(HERE, "_training.so")
+BINDING_ABI = os.path.join(OBJ, "_training.abi")   # binding_abi() when BINDING was built
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 NVCC_FLAGS = [
@@ -42,8 +44,20 @@ def _older(target: str, files) -> bool:
     return any(os.path.getmtime(s) > t for s in files)
 
 
+def binding_abi() -> str:
+    """What the native module is built against: the installed torch and this Python."""
+    return f"torch {importlib.metadata.version('torch')} {sysconfig.get_config_var('EXT_SUFFIX')}"
+
+
+def _binding_stale() -> bool:
+    if _older(BINDING, _included(BINDING_SRC)) or not os.path.exists(BINDING_ABI):
+        return True
+    with open(BINDING_ABI) as f:
+        return f.read() != binding_abi()
+
+
 def stale() -> bool:
-    return _older(LIB, sources()) or _older(BINDING, _included(BINDING_SRC))
+    return _older(LIB, sources()) or _binding_stale()
 
 
 def binding_command(out: str) -> list:
@@ -87,7 +101,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
             cmd.insert(1, "-Xptxas=-v")
             print(" ".join(cmd), flush=True)
         jobs.append((subprocess.Popen(cmd), cmd, tmp, obj))
-    if force or _older(BINDING, _included(BINDING_SRC)):
+    binding = force or _binding_stale()
+    if binding:
         tmp = BINDING + f".tmp{os.getpid()}"
         cmd = binding_command(tmp)
         jobs.append((subprocess.Popen(cmd), cmd, tmp, BINDING))
@@ -96,6 +111,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
         raise subprocess.CalledProcessError(1, failed[0])
     for _, _, tmp, obj in jobs:
         os.replace(tmp, obj)
+    if binding:
+        tmp = BINDING_ABI + f".tmp{os.getpid()}"
+        with open(tmp, "w") as f:
+            f.write(binding_abi())
+        os.replace(tmp, BINDING_ABI)
     if not force and not _older(LIB, objs):
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"

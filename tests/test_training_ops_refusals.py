@@ -59,3 +59,21 @@ def test_balance_and_its_scale_come_together(beam):
         layer.backward_checkpoint({}, dy, balance={})
     with pytest.raises(ValueError, match="balance_scale"):
         layer.backward_checkpoint({}, dy, balance_scale=0.5)
+
+
+def test_the_native_module_belongs_to_one_torch(monkeypatch):
+    """_training.so holds the installed torch's C++ ABI: under another torch or Python it is stale."""
+    import importlib.metadata
+    import sysconfig
+
+    from dynamic_expert_routing_b200 import build
+    build.build()
+    assert not build.stale()
+    version = importlib.metadata.version
+    with monkeypatch.context() as m:
+        m.setattr(importlib.metadata, "version", lambda name: "1.0" if name == "torch" else version(name))
+        assert build.stale()
+    with monkeypatch.context() as m:
+        m.setattr(sysconfig, "get_config_var", lambda name: ".cpython-30.so")
+        assert build.stale()
+    assert not build.stale()
