@@ -4,7 +4,8 @@ linear backward.  Every step runs in the library's kernels; the native module _t
 (csrc/binding.cpp) checks the tensors, allocates the outputs and calls the library.
 
 Each call runs on the current stream of its tensors' device, or on `stream` of that device, for which its
-outputs and scratch are then allocated; the tensors of a returned dict share one allocation.
+outputs and scratch are then allocated; the tensors of a returned dict share one allocation (a loss over
+packed sequences has its own).
 Tensors that a call cannot take raise ValueError (TypeError where a tensor is expected and
 something else given), a refusal by the library BeamError.
 """

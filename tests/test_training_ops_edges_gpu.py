@@ -226,3 +226,13 @@ def test_layer_calls_on_a_given_stream():
     for k, v in want.items():
         assert torch.equal(got[k], v), k
     torch.cuda.synchronize()
+
+
+def test_a_kept_loss_keeps_little_else():
+    b = beam()
+    logits, ids = rnd(0, 400, 60).cuda(), torch.zeros((400, 4), dtype=torch.int32, device="cuda")
+    cu = torch.arange(0, 401, 5, dtype=torch.int32, device="cuda")
+    out = b.balance_loss(logits, ids, cu_seqlens=cu)
+    assert out["prob"].shape == (80, 60)
+    assert out["loss"].untyped_storage().nbytes() <= 4096
+    assert b.balance_loss(logits, ids)["loss"].untyped_storage().nbytes() <= 4096
