@@ -444,13 +444,18 @@ static long long weight_bytes(const lin::Params& p)
     return slices > 1 ? slices * p.M * weight_ld(p.N) * 4 : 0;
 }
 
-static beam_status_t check_linear(int T, int C, int d, const void* g, int dtype, long long ldg)
+static beam_status_t check_sizes(int T, int C, int d)
 {
     if (T < 0 || T > (1 << 30)) FAIL_ARG("T=%d outside [0, 2^30]", T);
     if (C < 1 || C > kMaxLogits) FAIL_ARG("C=%d must be in [1, %d]", C, kMaxLogits);
     if (d < 1 || d > kMaxWidth) FAIL_ARG("d=%d must be in [1, %d]", d, kMaxWidth);
     if (ceil_div(T, lin::BM) * ceil_div(d, lin::kBN) > (1LL << 30))
         FAIL_ARG("T=%d rows of %d values are too many", T, d);
+    return BEAM_OK;
+}
+static beam_status_t check_linear(int T, int C, int d, const void* g, int dtype, long long ldg)
+{
+    TRY(check_sizes(T, C, d));
     return check_matrix("dlogits", g, dtype, false, T, C, ldg);
 }
 
@@ -483,7 +488,7 @@ extern "C" {
 
 int64_t beam_router_weight_grad_workspace(int32_t T, int32_t d, int32_t C)
 {
-    if (T < 0 || d < 1 || d > kMaxWidth || C < 1 || C > kMaxLogits) return -1;
+    if (check_sizes(T, C, d) != BEAM_OK) return -1;
     return T == 0 ? 0 : weight_bytes(weight_params(T, C, d));
 }
 

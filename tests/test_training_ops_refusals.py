@@ -77,3 +77,13 @@ def test_the_native_module_belongs_to_one_torch(monkeypatch):
         m.setattr(sysconfig, "get_config_var", lambda name: ".cpython-30.so")
         assert build.stale()
     assert not build.stale()
+
+
+def test_workspace_sizes_out_of_range(beam):
+    """-1 for every size that the call itself refuses."""
+    lib = beam.load()
+    assert lib.beam_router_weight_grad_workspace((1 << 30) + 1, 8, 6) == -1
+    assert lib.beam_router_weight_grad_workspace(1 << 30, 65536, 6) == -1     # too many tiles
+    assert lib.beam_router_weight_grad_workspace(4, 65537, 6) == -1
+    assert lib.beam_router_weight_grad_workspace(4, 8, (1 << 20) + 1) == -1
+    assert lib.beam_router_weight_grad_workspace(1 << 30, 32, 6) >= 0
