@@ -68,6 +68,20 @@ static cudaError_t with_type3(int dtype, F f)
     return with_type(dtype, f);
 }
 
+// SMs of the current device.
+static int num_sms()
+{
+    static std::atomic<int> cached[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+    n = cached[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
+        cached[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
 // ---------------------------------------------------------------- balance loss
 struct BalArgs {
     const void* logits; int dtype, T, E; long long ldl; const int32_t* topk; int K;
@@ -152,7 +166,7 @@ static cudaError_t launch_balance_grad(const BalArgs& a, const int32_t* counts, 
 {
     // as many CTAs as are resident (four per SM): 8192 x 212 with slots 8.9 us, with eight per SM 9.4, two 10.8
     const long long pass = (long long)kBalWarps * (32 / LPR);
-    const int run = (int)std::max(pass, ceil_div(ceil_div(a.T, 148 * 4), pass) * pass);
+    const int run = (int)std::max(pass, ceil_div(ceil_div(a.T, num_sms() * 4), pass) * pass);
     return launch_free(balance_grad_kernel<T, LPR>, dim3((unsigned)ceil_div(a.T, run)), dim3(kBalThreads), 0, st,
                        (const T*)a.logits, a.ldl, a.T, a.E, run, a.topk, a.K, a.valid, a.cu, a.n_seq, counts, tokens,
                        scale, dr, dl, out);
@@ -298,7 +312,8 @@ beam_status_t beam_checkpoint_route_grad(const int8_t* q, const uint8_t* scale, 
     const float reg = (float)((double)reg_scale / ((double)T * K));
     // warps per token: the fewest that give every SM 16 warps, as long as each has a strip of columns
     int wpt = 1;
-    while (wpt < kDotWarps && (long long)T * wpt < 148 * 16 && wpt * kDotCols < d) wpt *= 2;
+    const int enough = num_sms() * 16;
+    while (wpt < kDotWarps && (long long)T * wpt < enough && wpt * kDotCols < d) wpt *= 2;
     const bool grads = S == 1;
     BEAM_HOST_CUDA(with_type(dtype, [&](auto z) {
         using TY = decltype(z);
@@ -325,19 +340,6 @@ beam_status_t beam_checkpoint_route_grad(const int8_t* q, const uint8_t* scale, 
 
 // ---------------------------------------------------------------- the router's linear backward
 }  // extern "C"
-
-static int num_sms()
-{
-    static std::atomic<int> cached[64];
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
-    n = cached[dev].load(std::memory_order_relaxed);
-    if (n == 0) {
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
-        cached[dev].store(n, std::memory_order_relaxed);
-    }
-    return n;
-}
 
 // Slices of k: as many as fill the pairs of SMs, each of at least kChain steps.
 static void plan_slices(lin::Params& p, int pairs)

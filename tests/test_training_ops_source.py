@@ -44,3 +44,8 @@ def test_arrivals_in_another_cta_have_cluster_scope():
     issuer = lin[lin.index("kMmaWarp && rank == 0"):lin.index("tc_mma_f16_pair")]
     waits = re.findall(r"mbar_wait(<true>)?\((?:full|tempty)_bar", issuer)
     assert len(waits) == 2 and all(waits) and "fence_acquire_shared();" in issuer
+
+
+def test_launch_sizes_ask_the_device():
+    """The number of SMs is the device's (num_sms), not written out."""
+    assert not re.search(r"\b148\b", code("train_ops.cu"))
