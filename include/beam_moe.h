@@ -584,8 +584,10 @@ beam_status_t beam_checkpoint_route_grad(const int8_t *q_dev, const uint8_t *sca
  *   aligned, free again when the call's kernels are done.
  * beam_router_input_grad: dx_dev [T][d] float32, rows ld_dx elements apart, = dlogits W^T, w_dev [d][C]
  *   float32 or bfloat16, rows ld_w elements apart.
- * A dlogits or W value that is not finite makes the outputs it reaches NaN.  Both run on the
- * tensor cores with float32 accuracy; a bounded device wait that runs out sets the outputs to NaN.
+ * A dlogits or W value that is not finite leaves nothing finite in the outputs it reaches (those with a
+ * non-zero factor): NaN from a float32 operand, an infinity or NaN from a bfloat16 one.  Both run on the
+ * tensor cores with float32 accuracy; where a bounded device wait runs out, the tiles of that pair of CTAs
+ * that are not yet stored are set to NaN.
  */
 int64_t beam_router_weight_grad_workspace(int32_t T, int32_t d, int32_t C); /* -1: out of range */
 beam_status_t beam_router_weight_grad(const int8_t *q_dev, const uint8_t *scale_dev, int32_t T,

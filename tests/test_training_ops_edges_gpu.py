@@ -236,3 +236,36 @@ def test_a_kept_loss_keeps_little_else():
     assert out["prob"].shape == (80, 60)
     assert out["loss"].untyped_storage().nbytes() <= 4096
     assert b.balance_loss(logits, ids)["loss"].untyped_storage().nbytes() <= 4096
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_linear_backward_of_values_that_are_not_finite(dtype, bad):
+    """They reach their own row or column of the result, where nothing finite is left (NaN from a float32
+    operand, an infinity or NaN from a bfloat16 one); every other number is the one without them."""
+    b = beam()
+    T, D, C = 300, 200, 70
+    x, g, w = rnd(1, T, D).cuda(), rnd(2, T, C).to(dtype).cuda(), rnd(3, D, C).to(dtype).cuda()
+    x[x == 0] = 1
+    c = b.checkpoint_save(x)
+    dw, dx = b.router_weight_grad(c, g), b.router_input_grad(g, w)
+    gb, wb = g.clone(), w.clone()
+    gb[130, 65], wb[7, 3] = bad, bad
+
+    def check(got, want, reached):
+        assert not torch.isfinite(got[reached]).any()
+        if dtype == torch.float32 or bad != bad:
+            assert torch.isnan(got[reached]).all()
+        assert torch.equal(got[~reached], want[~reached])
+    at = torch.zeros((D, C), dtype=torch.bool, device="cuda")
+    at[:, 65] = b.checkpoint_load(c)[130] != 0
+    skip = ~at[:, 65]
+    got = b.router_weight_grad(c, gb)
+    got[skip, 65] = dw[skip, 65]                # 0 times an infinity: NaN or not, by the operand's type
+    check(got, dw, at)
+    at = torch.zeros((T, D), dtype=torch.bool, device="cuda")
+    at[130] = True
+    check(b.router_input_grad(gb, w), dx, at)
+    at = torch.zeros((T, D), dtype=torch.bool, device="cuda")
+    at[:, 7] = True
+    check(b.router_input_grad(g, wb), dx, at)
