@@ -81,7 +81,7 @@ WEIGHT = [
     (8192, 1536, 424, 0), (4500, 1530, 421, 1),
     # tiles of 64 columns: 16 tiles in 4 slices; 79 tiles, unsliced
     (8192, 4096, 16, 0), (700, 20000, 50, 2),
-    # one tile in 64 slices, the last step ragged
+    # one tile in 65 slices, the last step ragged
     (16390, 100, 100, 8),
 ]
 
