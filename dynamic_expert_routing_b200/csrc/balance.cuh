@@ -28,7 +28,7 @@
 // Measured on B200 (device time, L2 warm; the floor is the bytes read and written at the measured copy
 // rate): 64 tokens of 8 experts 3.0 us in one launch (two launches and a warp per row: 10.6);
 // 16384 x 60 bf16 in 24 sequences 12.4 us (floor 0.4: two dependent launches, each a chain of five or
-// six round trips to memory); 65536 x 60 float32 15 us (floor 2.6; with a warp per row and one CTA to
+// six round trips to memory; adding the runs through a cluster's shared memory in one launch is not built); 65536 x 60 float32 15 us (floor 2.6; with a warp per row and one CTA to
 // reduce: 164).  The gradient of 8192 x 212 with slot gradients 8.9 us (floor 3.4), of 65536 x 60 12.3 us
 // (floor 4.8): two fifths of the copy rate, the rest being the softmax's two chains of shuffles per row.
 #pragma once

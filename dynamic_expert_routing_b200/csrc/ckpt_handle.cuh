@@ -10,8 +10,9 @@ namespace beam {
 constexpr int kCkptHandleUnroll = 4;
 
 // Row t K + k of q / scale = Y_perm row inv[t][k], split-K slices added in slice order.  A thread takes 4
-// columns, 8 lanes a block; D is a multiple of 4.  HBM-bound: each output is read once (2 bytes per
-// value from the tensor-core path) and written in one byte.
+// columns, 8 lanes a block; D is a multiple of 4.  Each output is read once (2 bytes per value from the
+// tensor-core path) and written in one byte, but not at the copy rate: the 8-byte loads wait for the row's
+// place.  8192 tokens x 16 slots x 1536: 285 us with the routing's copies, 610 MB, 2.1 TB/s (floor 93 us).
 template <typename TY>
 __global__ void __launch_bounds__(kCkptThreads)
 ckpt_experts_kernel(const TY* __restrict__ yperm, int splits, long long stride, const int* __restrict__ inv,

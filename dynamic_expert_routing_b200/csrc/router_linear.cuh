@@ -32,11 +32,12 @@
 // Every wait is bounded: when one runs out, the pair's tiles that are not yet stored are set to NaN.
 //
 // Measured on B200 (device time):
-//   dW 8192 x 1536 x 424, float32 G: 38.6 us, 276 TFLOP/s of dW's own operations, 0.83 PFLOP/s with the limbs;
+//   dW 8192 x 1536 x 424, float32 G: 38.4 us, 278 TFLOP/s of dW's own operations, 0.83 PFLOP/s with the limbs;
 //     unsliced 92 us.  What bounds it is the loaders' work per step (converting and storing 40 KB per CTA):
-//     the MMAs alone take 20 of them.  1003 x 2048 x 128, bf16 G: 9.1 us (unsliced 12.2).
-//   dx 8192 x 2048 x 128, float32 G, bf16 W: 19.9 us, 67 MB written (floor 11 us at the copy rate); with A
-//     converted again for every n tile 34 us.  8192 x 1536 x 424 (A too long to stay): 55 us, bf16 G 24 us.
+//     the MMAs alone take 20 of them.  bf16 G 32 us.  1003 x 2048 x 128, bf16 G: 9.1 us (unsliced 11.6).
+//   dx 8192 x 2048 x 128, float32 G, bf16 W: 19.8 us, 67 MB written (floor 11 us at the copy rate); with A
+//     converted again for every n tile 34 us; float32 W 27.8.  8192 x 1536 x 424 (float32 G is too long to stay):
+//     55 us, W as [C][D] 52, float32 W 69, bf16 G and W 24.
 //   Error against 64 bits at 8192 x 1536 x 424: 1.1e-7; with the accumulator drained every 16 steps 2.1e-7,
 //     never 3.0e-6 (2.3e-6 of it towards zero), with one accumulator for all products 8.5e-7.
 #pragma once
@@ -334,7 +335,7 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t saddr)
 }
 
 // NARROW: tiles of 64 columns, for n <= 64 (MN-major B only: a share's 32 columns take the lower half of each
-// 128-byte row).  dW 4096 x 4096 x 16 14.5 us, with 128 columns 16.3.
+// 128-byte row).  dW 4096 x 4096 x 16 15.3 us, with 128 columns 16.5.
 template <int SA, bool MNA, int SB, bool MNB, bool VEC, bool RES, bool NARROW>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 lin_gemm_kernel(const __grid_constant__ Params p)
@@ -389,7 +390,7 @@ lin_gemm_kernel(const __grid_constant__ Params p)
     const uint32_t tmem_base = *tmem_slot;
     pdl_wait();
     // The next launch may begin now, behind this grid, where it is another operator's (input grad 64 x 256 x 16:
-    // 4.9 us against 5.8); lin_reduce_kernel's many CTAs, started early, cost the MMAs more than they gain.
+    // 5.2 us against 5.9); lin_reduce_kernel's many CTAs, started early, cost the MMAs more than they gain.
     if (p.last) pdl_launch_dependents();
 
     if (warp < kLoadWarps) {
@@ -582,7 +583,7 @@ lin_gemm_kernel(const __grid_constant__ Params p)
             // what the loaders (the first) and the epilogue (the second) have completed.  A release at cluster scope
             // alone orders the issuer behind another CTA's threads (a local arrival's ends with the CTA); a loader's
             // own would wait for the loads of its next step, these threads have none in flight: dW 8192 x 1536 x
-            // 424 38.6 us, with the loaders' own 42.  A phase is passed on before its barrier can complete the
+            // 424 38.4 us, with the loaders' own 42.  A phase is passed on before its barrier can complete the
             // next, which needs the MMAs behind this arrival.
             const bool steps = warp == kMmaWarp;
             int left = 0;
